@@ -564,6 +564,229 @@ QW_API qw_status qw_probe_stream_read(const void *p, int64_t bytes, uint32_t mag
                                       void *stream);
 QW_API qw_status qw_probe_shader_clock(uint64_t *out, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged int8 KV cache and its attention: what a decoder layer runs
+ * between its fused QKV GEMM and its output GEMM.
+ *
+ * The cache of one layer is four caller-owned buffers, in blocks of
+ * block_size tokens (16, 32, 64 or 128):
+ *
+ *   k_cache   int8 [num_blocks][kv_heads][block_size][head_dim]
+ *   v_cache   int8 [num_blocks][kv_heads][head_dim][block_size]
+ *   k_scales  fp32 [num_blocks][kv_heads]
+ *   v_scales  fp32 [num_blocks][kv_heads]
+ *
+ * A value is its code times the scale of its block and head: the symmetric
+ * method of the weights (bound -> 127, round half to even, clamp), with
+ * fp32 scales because bf16 activations have more range than an fp16 scale
+ * holds.  Values lie transposed within their block: that is the operand
+ * layout of the attention's second product.
+ *
+ * Token p of request r lies in slot block_table[r][p / block_size] *
+ * block_size + p % block_size; the table is int32 [requests][table_width].
+ *
+ * Types: `dtype` names the 16-bit activation type (qw_dtype).  head_dim is
+ * 64 or 128.  Activations are [tokens][heads][head_dim] with contiguous
+ * heads and a stride between tokens in elements (a multiple of 8), so that
+ * the column ranges of a fused QKV output can be passed as they are.
+ *
+ * Alignment: activations, caches, scales, tables of cos and sin, norm
+ * weights and workspaces 16 bytes; int32 arrays 4 bytes.
+ *
+ * Lengths, slots, positions and tables live on the device and are not
+ * visible to the host checks: the kernels bound every one of them and treat
+ * what lies outside as documented, never reading or writing outside the
+ * buffers that the arguments describe.  None of these calls waits for the
+ * device, so all of them can be captured into a graph.
+ * ------------------------------------------------------------------------- */
+
+typedef enum qw_dtype {
+    QW_F16 = 0, /* IEEE binary16 */
+    QW_BF16 = 1 /* bfloat16 */
+} qw_dtype;
+
+/* Most requests of one qw_kv_plan call (their running sums are held in LDS). */
+#define QW_KV_PLAN_MAX_REQUESTS 8191
+
+/*
+ * qw_kv_plan -- block tables and slot maps of one step, from request lengths.
+ *
+ * Request r holds past[r] tokens and adds fresh[r] (negative values count as
+ * 0).  With B = block_size it owns ceil(past / B) blocks, and takes
+ * ceil((past + fresh) / B) - ceil(past / B) more from free_blocks, in order:
+ * request by request, block by block.  Tokens are numbered request by
+ * request, in order; those beyond max_tokens are dropped (they get no slot
+ * and no block).
+ *
+ *   past, fresh   int32 [requests]
+ *   block_table   int32 [requests][table_width]: the entries of owned blocks
+ *                 are read, those of the blocks taken are written
+ *   free_blocks   int32 [n_free] ids to hand out; when they run out, the
+ *                 entries written are -1 and their tokens' slots are -1
+ *   cu_tokens     int32 [requests + 1] (written): the first token of each
+ *                 request, then their number
+ *   context       int32 [requests] (written): past + (fresh as kept)
+ *   positions     int32 [max_tokens] (written): position of each token in its
+ *                 request; -1 behind the last token
+ *   slots         int32 [max_tokens] (written): cache slot of each token; -1
+ *                 behind the last token, for a token whose block is missing
+ *                 (no free block, a negative table entry, a position beyond
+ *                 table_width * B), and for slots above 2^31 - 1
+ *   counts        int32 [2] (written): blocks the step takes (more than
+ *                 n_free: they ran out), tokens before dropping (more than
+ *                 max_tokens: some were dropped)
+ *
+ * Errors: QW_ERROR_INVALID_VALUE (null pointer where elements are needed,
+ * negative size, written buffers overlapping anything else),
+ * QW_ERROR_UNSUPPORTED (block_size not 16, 32, 64 or 128, requests above
+ * QW_KV_PLAN_MAX_REQUESTS, other sizes above 2^31 - 1), QW_ERROR_MISALIGNED,
+ * QW_ERROR_LAUNCH.  requests == 0 still writes cu_tokens[0] = 0, the counts
+ * and the padding of positions and slots.
+ */
+QW_API qw_status qw_kv_plan(const int32_t *past, const int32_t *fresh, int64_t requests,
+                            int32_t *block_table, int64_t table_width, const int32_t *free_blocks,
+                            int64_t n_free, int64_t block_size, int64_t max_tokens,
+                            int32_t *cu_tokens, int32_t *context, int32_t *positions,
+                            int32_t *slots, int32_t *counts, void *stream);
+
+/*
+ * qw_qk_norm_rope -- RMS norm of each query and key head and the rotation by
+ * position, in one pass, in fp32, rounded once:
+ *
+ *   y = x * w / sqrt(mean(x^2) + eps)                 (null weights: y = x)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
+ *
+ * for the pairs (a, b) of the first rot_dim channels: (2 i, 2 i + 1) if
+ * interleaved, else (i, i + rot_dim / 2), with cos[position][i] and
+ * sin[position][i]; the other channels are not rotated.
+ *
+ *   q, k          [tokens][heads][head_dim], q_stride and k_stride elements
+ *                 between tokens
+ *   positions     int32 [tokens]; a position outside [0, max_position) gives
+ *                 a row of zeros (padding)
+ *   cos, sin      fp32 [max_position][rot_dim / 2]
+ *   rot_dim       0 to head_dim, a multiple of 16
+ *   q_weight, k_weight   [head_dim] of the same dtype; both or neither null
+ *   q_out, k_out  (written) with strides of their own; an output may be its
+ *                 input (same pointer and stride)
+ *
+ * Errors: QW_ERROR_INVALID_VALUE (null pointer, negative size, a stride
+ * below heads * head_dim, one null weight, outputs overlapping anything else
+ * than their own input, unknown dtype, eps negative or not finite),
+ * QW_ERROR_UNSUPPORTED (head_dim, rot_dim,
+ * strides not a multiple of 8, tokens * heads * head_dim above 2^38, more
+ * than 2^31 - 1 tokens), QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.
+ */
+QW_API qw_status qw_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                 int dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                                 int64_t head_dim, const int32_t *positions, const float *cos,
+                                 const float *sin, int64_t max_position, int64_t rot_dim,
+                                 int interleaved, const void *q_weight, const void *k_weight,
+                                 double eps, void *q_out, int64_t q_out_stride, void *k_out,
+                                 int64_t k_out_stride, void *stream);
+
+/*
+ * qw_kv_write -- quantize new keys and values into the cache.
+ *
+ * The tokens of one call that fall into one block have to follow each other
+ * with consecutive slots (as qw_kv_plan numbers them): a run.  Per run and
+ * head, with `off` the run's first offset in its block,
+ *
+ *   S' = fp32(max|x| / 127) over the run           (0 where below 2^-100)
+ *   S  = off > 0 ? max(S_old, S') : S'
+ *   q  = clamp(round_half_even(fp32(x / S)), -127, 127)       (S = 0: 0)
+ *
+ * and, where S > S_old, the codes of the block's tokens before the run move
+ * to the new scale: q = round_half_even(fp32(q * fp32(S_old / S))).  A run at
+ * offset 0 starts its block afresh.  Codes and scales are bit-exact by
+ * contract for finite inputs (others give unspecified codes and scales).
+ *
+ *   k, v     [tokens][kv_heads][head_dim], k_stride and v_stride elements
+ *            between tokens
+ *   slots    int32 [tokens]; a slot outside [0, num_blocks * block_size)
+ *            skips its token
+ *
+ * Errors: QW_ERROR_INVALID_VALUE (null pointer, negative size, a stride
+ * below kv_heads * head_dim, cache buffers overlapping each other or an
+ * input, unknown dtype), QW_ERROR_UNSUPPORTED (head_dim, block_size, strides
+ * not a multiple of 8, kv_heads above 65535, tokens or num_blocks above
+ * 2^31 - 1), QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.  tokens == 0 is a no-op.
+ */
+QW_API qw_status qw_kv_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                             int dtype, int64_t tokens, int64_t kv_heads, int64_t head_dim,
+                             const int32_t *slots, int8_t *k_cache, int8_t *v_cache,
+                             float *k_scales, float *v_scales, int64_t num_blocks,
+                             int64_t block_size, void *stream);
+
+/*
+ * qw_kv_read -- the values that slots of the cache stand for: code * scale,
+ * rounded to `dtype`; zeros for a slot outside the cache.
+ *
+ *   slots   int32 [tokens]
+ *   k, v    [tokens][kv_heads][head_dim], contiguous (written)
+ *
+ * Errors: as qw_kv_write.
+ */
+QW_API qw_status qw_kv_read(const int32_t *slots, int64_t tokens, const int8_t *k_cache,
+                            const int8_t *v_cache, const float *k_scales, const float *v_scales,
+                            int64_t num_blocks, int64_t block_size, int64_t kv_heads,
+                            int64_t head_dim, int dtype, void *k, void *v, void *stream);
+
+/*
+ * qw_kv_attention -- attention of new queries over the cache.
+ *
+ * Request r has context[r] tokens in the cache and the query tokens
+ * cu_tokens[r] .. cu_tokens[r + 1] - 1, its last ones: query i of n stands at
+ * position p = context - n + i and attends to the keys j < context with
+ * j <= p (if causal) and j > p - window (if window > 0):
+ *
+ *   out = sum_j softmax_j(scale * q . K_j) V_j
+ *
+ * A row that attends to nothing gives zeros.  Query head h uses key head
+ * h / (q_heads / kv_heads).  Scores, the softmax's maximum and sum and the
+ * output are accumulated in fp32; softmax weights are rounded to fp16 for the
+ * second product; codes are exact.
+ *
+ *   q            [tokens][q_heads][head_dim], q_stride elements between tokens
+ *   context      int32 [requests], taken as at most max_context
+ *   cu_tokens    int32 [requests + 1], not decreasing; values are taken as
+ *                within [0, tokens], and of a request's queries the first
+ *                max_new are computed
+ *   block_table  int32 [requests][table_width]; the keys of a block id outside
+ *                [0, num_blocks) are not attended to
+ *   max_new      at least the most queries of a request
+ *   max_context  at least the longest context (table_width * block_size at
+ *                most is used); it sizes the grid
+ *   scale        multiplies the scores (usually head_dim^-1/2)
+ *   out          [tokens][q_heads][head_dim], contiguous (written); rows that
+ *                belong to no request keep what they hold
+ *   workspace    qw_kv_attention_workspace() bytes (may be null if that is 0)
+ *
+ * Errors: QW_ERROR_INVALID_VALUE (null pointer, negative size, a workspace
+ * that is too small, scale not finite, q_heads not a multiple of kv_heads,
+ * a stride below q_heads * head_dim, out or workspace overlapping an input
+ * or each other, unknown dtype), QW_ERROR_UNSUPPORTED (head_dim, block_size,
+ * stride not a multiple of 8, requests above 65535, max_new * q_heads above
+ * 2^20, other sizes above 2^31 - 1), QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.
+ * tokens == 0 or requests == 0 is a no-op.
+ *
+ * qw_kv_attention_workspace -- workspace bytes for these sizes on any device
+ * (0: none needed), -1 for sizes that the call rejects.
+ */
+QW_API qw_status qw_kv_attention(const void *q, int64_t q_stride, int dtype, int64_t tokens,
+                                 int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                 const int8_t *k_cache, const int8_t *v_cache,
+                                 const float *k_scales, const float *v_scales, int64_t num_blocks,
+                                 int64_t block_size, const int32_t *block_table,
+                                 int64_t table_width, const int32_t *context,
+                                 const int32_t *cu_tokens, int64_t requests, int64_t max_new,
+                                 int64_t max_context, double scale, int causal, int64_t window,
+                                 void *out, void *workspace, int64_t workspace_bytes, void *stream);
+QW_API int64_t qw_kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                                         int64_t head_dim, int64_t block_size,
+                                         int64_t table_width, int64_t requests, int64_t max_new,
+                                         int64_t max_context, int64_t window);
+
 /* A static, human-readable name for a status code (never NULL). */
 QW_API const char *qw_status_string(qw_status status);
 

@@ -16,12 +16,19 @@ Names follow the pages: symmetric per-channel int8 weight quantization with
 an optional percentage clip (LightSeq slide deck, "量化流程" and
 "量化：裁剪+对称") and the W8A16 MatMul whose right operand is the int8
 weight ("探索ChatGLM2在算能BM1684X上INT8量化部署", sections 2-4).
+
+What a decoder layer runs between its GEMMs is here too, around a paged int8
+KV cache (kv.py): kv_plan, qk_norm_rope, kv_write, kv_read, kv_attention.
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
+
+from . import kv as _kv
+from .kv import (KV_BLOCK_SIZES, KV_HEAD_DIMS, KV_PLAN_MAX_REQUESTS, KvCache, KvPlan, kv_attention,
+                 kv_attention_workspace, kv_cache, kv_plan, kv_read, kv_write, qk_norm_rope)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # QW_LIBRARY names another build of the same library (the CPU tests load a
@@ -129,6 +136,7 @@ def _load():
     lib.qw_probe_stream_read.restype = ctypes.c_int
     lib.qw_probe_shader_clock.argtypes = [vp, vp]
     lib.qw_probe_shader_clock.restype = ctypes.c_int
+    _kv._declare(lib)
     lib.qw_version.argtypes = []
     lib.qw_version.restype = ctypes.c_int
     _lib_handle = lib
@@ -585,4 +593,6 @@ __all__ = ["quantize_weights", "quantize_weights_fixed_range", "quantize_weights
            "status_string", "version", "library", "auto_path", "mfma_tile", "w8a8_tile",
            "quantize_weights_raw", "quantize_weights_f16_raw", "quantize_weights_fixed_range_raw", "quantize_weights_asym_raw", "w8a16_gemm_asym_raw",
            "quantize_weights_outliers_raw", "w8a16_gemm_outliers_raw", "w8a16_gemm_raw", "w8a8_gemm_raw",
-           "probe_stream_read_raw", "probe_shader_clock_raw", "PATHS", "LIBRARY_PATH"]
+           "probe_stream_read_raw", "probe_shader_clock_raw", "PATHS", "LIBRARY_PATH",
+           "KvCache", "KvPlan", "kv_cache", "kv_plan", "qk_norm_rope", "kv_write", "kv_read", "kv_attention",
+           "kv_attention_workspace", "KV_HEAD_DIMS", "KV_BLOCK_SIZES", "KV_PLAN_MAX_REQUESTS"]

@@ -6,8 +6,8 @@ Each translation unit is compiled with hipcc for gfx950 only, then linked
 into ``int8_weight_quantized_amd/libqw.so``.  Flags worth knowing:
   * ``-Xclang -target-feature -Xclang -packed-fp32-ops`` keeps the compiler
     from emitting packed fp32 VALU instructions (harmless host-pass warning);
-  * ``-ffp-contract=off`` on the quantizer and the C ABI unit: the rounding
-    contract of the quantizer forbids fused multiply-add;
+  * ``-ffp-contract=off`` on the quantizers (weights and KV cache) and the C
+    ABI unit: the rounding contract of the quantizers forbids fused multiply-add;
   * no fast-math anywhere; fp32 division stays correctly rounded (hipcc's
     default -fhip-fp32-correctly-rounded-divide-sqrt).
 """
@@ -43,6 +43,11 @@ UNITS = {
     "gemm_skinny.hip": [],
     "tune.hip": [],
     "probe.hip": [],
+    "kv_api.hip": [],
+    "kv_plan.hip": [],
+    "qk_norm_rope.hip": [],
+    "kv_cache.hip": ["-ffp-contract=off"],
+    "kv_attention.hip": [],
 }
 
 
