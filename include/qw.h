@@ -770,8 +770,8 @@ QW_API qw_status qw_kv_read(const int32_t *slots, int64_t tokens, const int8_t *
  * 2^20, other sizes above 2^31 - 1), QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.
  * tokens == 0 or requests == 0 is a no-op.
  *
- * qw_kv_attention_workspace -- workspace bytes for these sizes on any device
- * (0: none needed), -1 for sizes that the call rejects.
+ * qw_kv_attention_workspace -- workspace bytes for these sizes on the current
+ * device (0: none needed), -1 for sizes that the call rejects.
  */
 QW_API qw_status qw_kv_attention(const void *q, int64_t q_stride, int dtype, int64_t tokens,
                                  int64_t q_heads, int64_t kv_heads, int64_t head_dim,

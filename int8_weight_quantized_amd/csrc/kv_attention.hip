@@ -32,34 +32,59 @@ namespace qw {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256; // of the join
 constexpr int kTile = 64; // keys a wave takes at once
 constexpr float kLazy = 8.0f;
+// What beginning and ending a unit costs a workgroup, in tiles: a workgroup
+// whose range spans several units is given fewer keys.  (0, 4 and 8: 34.3,
+// 32.9 and 33.4 us for 64 requests of 512 to 8192 keys, 38.0, 28.0 and 28.3 us
+// for 48 of 128 to 2048 with 16 key heads.)
+constexpr int kUnitCost = 4;
+constexpr int kMinRange = 4 + kUnitCost; // of a workgroup's range, at least
+
+constexpr int kWaves = 4; // of a split workgroup
+
+// Ranges a CU.  Two keep its memory pipe full where a tile is 16 KiB; with
+// tiles of 8 KiB and one row tile three do better (24.9 us against 28.0 for
+// 48 requests of 128 to 2048 keys, 16 key heads of 64 channels), while at 128
+// channels three are slower (33.2 against 32.9 us for 64 requests of 512 to
+// 8192 keys; 95 against 74 us with two row tiles): the older workgroups of a
+// CU are served first, and the youngest ends alone.
+constexpr int split_groups(int head_dim, int row_tiles) { return head_dim == 64 && row_tiles == 1 ? 3 : 2; }
+
+// Where the 64 keys of a tile lie.
+enum Layout {
+    kNarrow = 0, // in several blocks
+    kWhole = 1,  // in one block of 64
+    kHalf = 2    // in one block of 128: a value row of the tile is half a cache line
+};
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// What a block of query rows of one request attends to.
-struct Span {
+// What one request asks for.
+struct Request {
     int t0, past; // first token; cached tokens before it (negative where there are more queries than cached tokens)
     int ctx;      // cached tokens
     int rows;     // query rows of a key head: those of at most max_new tokens
-    int lo, hi;   // keys any of the rows [row0, row0 + count) sees; lo is a multiple of kTile
+    int lo, hi;   // keys that any of the rows sees; lo is a multiple of kTile
+    int cost;     // kTile-key tiles of that range, at least one, and kUnitCost; 0 without rows
 };
 
-__device__ __forceinline__ Span span_of(const KvAttnArgs &a, int r, int row0, int count)
+__device__ __forceinline__ Request request_of(const KvAttnArgs &a, int r)
 {
-    Span s;
+    Request s;
     s.t0 = clampi(a.cu_tokens[r], 0, a.tokens);
     const int n = clampi(a.cu_tokens[r + 1], s.t0, a.tokens) - s.t0;
+    const int queries = n < a.max_new ? n : a.max_new;
     s.ctx = clampi(a.context[r], 0, a.max_context);
     s.past = s.ctx - n;
-    s.rows = (n < a.max_new ? n : a.max_new) * a.group;
+    s.rows = queries * a.group;
     s.lo = s.hi = 0;
-    if (row0 < s.rows) {
-        const int end = row0 + count < s.rows ? row0 + count : s.rows;
-        const int first = row0 / a.group, last = (end - 1) / a.group;
-        s.hi = a.causal ? clampi(s.past + last + 1, 0, s.ctx) : s.ctx;
-        s.lo = a.window ? clampi(s.past + first - a.window + 1, 0, s.hi) & ~(kTile - 1) : 0;
+    s.cost = 0;
+    if (queries) {
+        s.hi = a.causal ? clampi(s.past + queries, 0, s.ctx) : s.ctx;
+        s.lo = a.window ? clampi(s.past - a.window + 1, 0, s.hi) & ~(kTile - 1) : 0;
+        s.cost = (s.hi > s.lo ? (s.hi - s.lo + kTile - 1) / kTile : 1) + kUnitCost;
     }
     return s;
 }
@@ -91,9 +116,9 @@ __device__ __forceinline__ void row_power(float top, float &up, float &down)
 }
 
 // ---------------------------------------------------------------------------
-// Split kernel: one workgroup for a chunk of the context, a key head and a
-// block of 16 RT query rows; its four waves take the chunk's 64-key tiles in
-// turn and are joined through LDS at the end.
+// Split kernel: the 64-key tiles of a unit (one key head and block of 16 RT
+// query rows of one request) are taken in turn by the waves of a workgroup,
+// which are joined through LDS at the end of the unit.
 //
 // S^T = Kq Q^T and O^T = Vq^T P^T on v_mfma_f32_16x16x32_f16.  A lane holds
 // column (query row) lane & 15 of S^T; which keys its registers hold depends
@@ -104,40 +129,89 @@ __device__ __forceinline__ void row_power(float top, float &up, float &down)
 // Nothing passes through LDS or between lanes but the row maximum.
 //
 // Bound by HBM: 2 * D + 8 / B bytes a key and head, each read once, straight
-// into registers; a tile is D / 4 16-byte loads in flight a lane.
+// into registers, past the caches (6.0 against 5.6 TB/s on long contexts).  A
+// tile is D / 4 loads of 16 bytes a lane in flight; asking for the next tile
+// before this one's products gained nothing, with eight waves a CU.
 // ---------------------------------------------------------------------------
-template <int D, int RT, int DT, bool WIDE /* a tile lies in one block */>
-__global__ __launch_bounds__(kThreads, RT == 1 ? 3 : 2) void kv_split_kernel(KvAttnArgs a, int chunk, int chunks)
+template <int D, int RT>
+struct SplitLds {
+    float o[kWaves][16 * RT][D + 4];
+    float m[kWaves][16 * RT], l[kWaves][16 * RT];
+};
+
+// Floats of an unfinished piece in the workspace: 16 RT rows of D channels,
+// the reference M, the denominator, and two of padding.
+constexpr int piece_floats(int head_dim, int row_tiles) { return 16 * row_tiles * (head_dim + 4); }
+
+// Tiles of one unit.
+struct Piece {
+    Request s;
+    int r, kvh, row0;
+    int begin, end; // keys
+    float *part;    // where it is left unfinished; null: it is the whole unit
+};
+
+// A workgroup's range, handed out piece by piece.  The units of all requests
+// lie in a row, request by request, each as long as its cost: kUnitCost, then
+// its tiles.
+struct Range {
+    int begin, at, stop;
+    Request s;   // request r; the requests before it cost `before` a unit
+    int r, before;
+    float *parts; // room for two pieces: one at the range's begin, one at its end
+
+    template <int D, int RT>
+    __device__ __forceinline__ bool next(const KvAttnArgs &a, int units, Piece &p)
+    {
+        while (at < stop) {
+            if (at >= (before + s.cost) * units) {
+                before += s.cost;
+                s = request_of(a, ++r);
+                continue;
+            }
+            const int rel = at - before * units;
+            const int unit = rel / s.cost, from = rel - unit * s.cost;
+            const int count = s.cost - from < stop - at ? s.cost - from : stop - at;
+            const int off = from > kUnitCost ? from - kUnitCost : 0, tiles = from + count - kUnitCost - off;
+            const int rb = unit / a.kv_heads;
+            p.s = s;
+            p.r = r;
+            p.kvh = unit - rb * a.kv_heads;
+            p.row0 = rb * 16 * RT;
+            p.begin = s.lo + off * kTile;
+            p.end = s.hi - p.begin < tiles * kTile ? s.hi : p.begin + tiles * kTile;
+            p.part = tiles == s.cost - kUnitCost ? nullptr : (at == begin ? parts : parts + piece_floats(D, RT));
+            at += count;
+            if (tiles > 0 && p.row0 < s.rows)
+                return true;
+        }
+        return false;
+    }
+};
+
+template <int D, int RT, int DT, int LAYOUT>
+__device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p, SplitLds<D, RT> &lds)
 {
-    constexpr int CH = D / 64;  // 64-channel pieces of a key row
+    constexpr int CH = D / 64; // 64-channel pieces of a key row
     constexpr int DTILES = D / 16;
-    constexpr int PITCH = D + 4;
-    __shared__ __attribute__((aligned(16))) float lds_o[4 * 16 * PITCH];
-    __shared__ float lds_m[4][16 * RT], lds_l[4][16 * RT];
+    constexpr int NW = kWaves;
 
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    const int kvh = blockIdx.y % a.kv_heads, rb = blockIdx.y / a.kv_heads, r = blockIdx.z;
-    const int row0 = rb * 16 * RT;
-    const Span s = span_of(a, r, row0, 16 * RT);
-    if (row0 >= s.rows)
-        return;
-    const int begin = s.lo + (int)blockIdx.x * chunk;
-    if (begin >= s.hi && blockIdx.x > 0)
-        return;
-    const int end = s.hi - begin < chunk ? s.hi : begin + chunk;
+    const int shift = LAYOUT == kWhole ? 6 : (LAYOUT == kHalf ? 7 : a.block_shift);
+    const int block = 1 << shift;
+    const int64_t head_bytes = (int64_t)block * D;
 
     // query rows, as the first product's second operand
     half8_t q[RT][CH][2];
     float mult[RT]; // scores -> exponents of 2, without the key scale
     int lim_lo[RT], lim_hi[RT];
-    const int past = s.past;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        const int row = row0 + t * 16 + col;
-        const bool in = row < s.rows;
-        const int i = in ? row / a.group : 0, head = kvh * a.group + (in ? row - i * a.group : 0);
-        const uint16_t *src = a.q + (int64_t)(s.t0 + i) * a.q_stride + (int64_t)head * D + g * 16;
+        const int row = p.row0 + t * 16 + col;
+        const bool in = row < p.s.rows;
+        const int i = in ? row / a.group : 0, head = p.kvh * a.group + (in ? row - i * a.group : 0);
+        const uint16_t *src = a.q + (int64_t)(p.s.t0 + i) * a.q_stride + (int64_t)head * D + g * 16;
         u32x4_t raw[CH][2];
         float top = 0.0f;
 #pragma unroll
@@ -162,13 +236,17 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? 3 : 2) void kv_split_kernel(KvA
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 q[t][c][h] = to_half8<DT>(raw[c][h], up);
-        lim_hi[t] = in ? (a.causal ? past + i + 1 : s.ctx) : 0;
-        lim_lo[t] = a.window ? past + i - a.window + 1 : 0;
+        lim_hi[t] = in ? (a.causal ? p.s.past + i + 1 : p.s.ctx) : 0;
+        lim_lo[t] = a.window ? p.s.past + i - a.window + 1 : 0;
     }
     // keys that every row of the block sees
-    const int last_row = row0 + 16 * RT < s.rows ? row0 + 16 * RT - 1 : s.rows - 1;
-    const int all_hi = a.causal ? past + row0 / a.group + 1 : s.ctx;
-    const int all_lo = a.window ? past + last_row / a.group - a.window + 1 : 0;
+    const int last_row = p.row0 + 16 * RT < p.s.rows ? p.row0 + 16 * RT - 1 : p.s.rows - 1;
+    const int all_hi = a.causal ? p.s.past + p.row0 / a.group + 1 : p.s.ctx;
+    const int all_lo = a.window ? p.s.past + last_row / a.group - a.window + 1 : 0;
+    // keys that some row of the block sees, of the piece's
+    const int any_hi = a.causal ? p.s.past + last_row / a.group + 1 : p.s.ctx;
+    const int any_lo = a.window ? (p.s.past + p.row0 / a.group - a.window + 1) & ~(kTile - 1) : 0;
+    const int begin = p.begin > any_lo ? p.begin : any_lo, end = p.end < any_hi ? p.end : any_hi;
 
     float4_t o[RT][DTILES];
     float m[RT], l[RT];
@@ -181,47 +259,46 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? 3 : 2) void kv_split_kernel(KvA
             o[t][d] = (float4_t){0, 0, 0, 0};
     }
 
-    const int32_t *table = a.block_table + (int64_t)r * a.table_width;
-    const int block = 1 << a.block_shift;
-    const int64_t head_bytes = (int64_t)block * D;
-    // Cache block that holds key j (0 where the table holds none: it is read
-    // in its place and masked).
-    auto block_of = [&](int j, bool &ok) {
-        int32_t id = j < s.hi ? table[j >> a.block_shift] : -1;
+    const int32_t *table = a.block_table + (int64_t)p.r * a.table_width;
+    // Cache row (block and head) that holds key j; block 0's where the table
+    // holds none: it is read in its place and masked.
+    auto row_of = [&](int j, bool &ok) {
+        const int32_t id = j < end ? table[j >> shift] : -1;
         ok = id >= 0 && id < a.num_blocks;
-        return (int64_t)(ok ? id : 0) * a.kv_heads + kvh;
+        return (int64_t)(ok ? id : 0) * a.kv_heads + p.kvh;
     };
 
-    u32x4_t kraw[4][CH], vraw[DTILES];
-    float ks, vs;
-    bool ok;
-    auto load = [&](int base) {
-        // key rows: row c of 16-key product i is key 16 (c / 4) + 4 i + c % 4
+    for (int base = begin + wave * kTile; base < end; base += NW * kTile) {
+        // Key rows: row c of 16-key product i is key 16 (c / 4) + 4 i + c % 4.
+        u32x4_t kraw[4][CH], vraw[DTILES];
+        bool ok;
         int64_t kb, vb;
-        if (WIDE) {
-            kb = vb = block_of(base, ok);
+        if (LAYOUT != kNarrow) {
+            kb = vb = row_of(base, ok);
         } else {
             bool unused;
-            kb = block_of(base + (col >> 2) * 16, unused);
-            vb = block_of(base + g * 16, ok);
+            kb = row_of(base + (col >> 2) * 16, unused);
+            vb = row_of(base + g * 16, ok);
         }
-        const int8_t *kp = a.k_cache + kb * head_bytes +
-                           (int64_t)(((base + (col >> 2) * 16) & (block - 1)) + (col & 3)) * D + g * 16;
-        const int8_t *vp = a.v_cache + vb * head_bytes + (int64_t)col * block + ((base + g * 16) & (block - 1));
-        ks = a.k_scales[vb];
-        vs = a.v_scales[vb];
+        const uint32_t k_at = (uint32_t)(((base + (col >> 2) * 16) & (block - 1)) + (col & 3)) * D + g * 16;
+        const uint32_t v_at = (uint32_t)(col * block + ((base + g * 16) & (block - 1)));
+        const int8_t *kp = a.k_cache + kb * head_bytes + k_at;
+        const int8_t *vp = a.v_cache + vb * head_bytes + v_at;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                kraw[i][c] = *reinterpret_cast<const u32x4_t *>(kp + i * 4 * D + c * 64);
+                kraw[i][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(kp + i * 4 * D + c * 64));
+        const float ks = a.k_scales[vb], vs = a.v_scales[vb];
 #pragma unroll
-        for (int d = 0; d < DTILES; ++d)
-            vraw[d] = *reinterpret_cast<const u32x4_t *>(vp + (int64_t)d * 16 * block);
-    };
+        for (int d = 0; d < DTILES; ++d) {
+            // (half a line is not streamed past the caches: the other half follows)
+            if (LAYOUT == kHalf)
+                vraw[d] = *reinterpret_cast<const u32x4_t *>(vp + d * 16 * block);
+            else
+                vraw[d] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(vp + d * 16 * block));
+        }
 
-    for (int base = begin + wave * kTile; base < end; base += 4 * kTile) {
-        load(base);
         float4_t sc[RT][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -243,7 +320,7 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? 3 : 2) void kv_split_kernel(KvA
         const float vsc = fmaxf(vs, kKvScaleFloor);
         const float lv = ok ? __log2f(vsc) : 0.0f;
         const float inv = ok ? 1.0f / vsc : 0.0f;
-        half8_t p[RT][2];
+        half8_t w[RT][2];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const float c = ok ? mult[t] * ks : 0.0f;
@@ -277,9 +354,9 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? 3 : 2) void kv_split_kernel(KvA
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float w = __builtin_amdgcn_exp2f(x[e] - ref);
-                sum += w;
-                p[t][e >> 3][e & 7] = (_Float16)w; // to nearest: 2^-12 of a weight
+                const float y = __builtin_amdgcn_exp2f(x[e] - ref);
+                sum += y;
+                w[t][e >> 3][e & 7] = (_Float16)y; // to nearest: 2^-11 of a weight at most
             }
             l[t] = fmaf(sum, inv, l[t]);
         }
@@ -289,119 +366,261 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? 3 : 2) void kv_split_kernel(KvA
             const half8_t v1 = i8x8_to_half8(vraw[d].z, vraw[d].w);
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[t][0], o[t][d], 0, 0, 0);
-                o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[t][1], o[t][d], 0, 0, 0);
+                o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[t][0], o[t][d], 0, 0, 0);
+                o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[t][1], o[t][d], 0, 0, 0);
             }
         }
     }
 
-    // join the waves, one 16-row tile at a time
+    // join the waves
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         l[t] = add_xor32(add_xor16(l[t]));
         if (g == 0) {
-            lds_m[wave][t * 16 + col] = m[t];
-            lds_l[wave][t * 16 + col] = l[t];
+            lds.m[wave][t * 16 + col] = m[t];
+            lds.l[wave][t * 16 + col] = l[t];
         }
-    }
-    __syncthreads();
-    const int valid = (s.hi - s.lo + chunk - 1) / chunk; // chunks of this row block
-    const bool final = valid <= 1;
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        float ref = lds_m[0][t * 16 + col];
-#pragma unroll
-        for (int w = 1; w < 4; ++w)
-            ref = fmaxf(ref, lds_m[w][t * 16 + col]);
-        const float f = m[t] == ref ? 1.0f : __builtin_amdgcn_exp2f(m[t] - ref);
 #pragma unroll
         for (int d = 0; d < DTILES; ++d)
-            *reinterpret_cast<float4_t *>(lds_o + (wave * 16 + col) * PITCH + d * 16 + g * 4) = o[t][d] * f;
-        __syncthreads();
-        // 16 threads a row, D / 16 channels each
-        const int row = (int)threadIdx.x >> 4, d0 = ((int)threadIdx.x & 15) * (D / 16);
-        float rm = lds_m[0][t * 16 + row], rl = 0.0f;
+            *reinterpret_cast<float4_t *>(&lds.o[wave][t * 16 + col][d * 16 + g * 4]) = o[t][d];
+    }
+    __syncthreads();
 #pragma unroll
-        for (int w = 1; w < 4; ++w)
-            rm = fmaxf(rm, lds_m[w][t * 16 + row]);
+    for (int t = 0; t < RT; ++t) {
+        // 16 threads a row, E channels each
+        constexpr int E = D / 16;
+        const int row = t * 16 + ((int)threadIdx.x >> 4), d0 = ((int)threadIdx.x & 15) * E;
+        float ref = lds.m[0][row];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float mw = lds_m[w][t * 16 + row];
-            rl += lds_l[w][t * 16 + row] * (mw == rm ? 1.0f : __builtin_amdgcn_exp2f(mw - rm));
-        }
-        float acc[D / 16];
+        for (int w = 1; w < NW; ++w)
+            ref = fmaxf(ref, lds.m[w][row]);
+        float sum = 0.0f, acc[E];
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
+        for (int e = 0; e < E; ++e)
             acc[e] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-                acc[e] += lds_o[(w * 16 + row) * PITCH + d0 + e];
+        for (int w = 0; w < NW; ++w) {
+            const float mw = lds.m[w][row];
+            const float f = mw == ref ? 1.0f : __builtin_amdgcn_exp2f(mw - ref);
+            sum = fmaf(lds.l[w][row], f, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] = fmaf(lds.o[w][row][d0 + e], f, acc[e]);
         }
-        const int gr = row0 + t * 16 + row;
-        if (gr < s.rows) {
-            if (final) {
-                const int i = gr / a.group, head = kvh * a.group + gr - i * a.group;
-                const float n = rl == 0.0f ? 0.0f : 1.0f / rl;
-                uint32_t *out = reinterpret_cast<uint32_t *>(a.out + ((int64_t)(s.t0 + i) * a.q_heads + head) * D + d0);
+        const int gr = p.row0 + row;
+        if (gr < p.s.rows) {
+            if (!p.part) {
+                const int i = gr / a.group, head = p.kvh * a.group + gr - i * a.group;
+                const float n = sum == 0.0f ? 0.0f : 1.0f / sum;
+                uint16_t *out = a.out + ((int64_t)(p.s.t0 + i) * a.q_heads + head) * D + d0;
 #pragma unroll
-                for (int e = 0; e < D / 16; e += 2)
-                    out[e / 2] = Act<DT>::pack(acc[e] * n, acc[e + 1] * n);
+                for (int e = 0; e < E; e += 2)
+                    *reinterpret_cast<uint32_t *>(out + e) = Act<DT>::pack(acc[e] * n, acc[e + 1] * n);
             } else {
-                const int64_t part =
-                    (((int64_t)r * gridDim.y + blockIdx.y) * chunks + blockIdx.x) * (16 * RT) + t * 16 + row;
-                float *w = a.workspace + part * (D + 4); // D channels, then M and the denominator
+                float *w = p.part + row * (D + 4);
 #pragma unroll
-                for (int e = 0; e < D / 16; e += 4)
+                for (int e = 0; e < E; e += 4)
                     *reinterpret_cast<float4_t *>(w + d0 + e) = (float4_t){acc[e], acc[e + 1], acc[e + 2], acc[e + 3]};
                 if (d0 == 0) {
-                    w[D] = rm;
-                    w[D + 1] = rl;
+                    w[D] = ref;
+                    w[D + 1] = sum;
                 }
             }
         }
-        if (t + 1 < RT)
-            __syncthreads();
     }
+    __syncthreads();
 }
 
-// Joins the chunks of a row: one wave a row, its lanes over the channels.
+// One workgroup a unit: for contexts that one workgroup reads fast enough,
+// or units enough to fill the chip many times over.
+template <int D, int RT, int DT, int LAYOUT>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a, int units)
+{
+    __shared__ __attribute__((aligned(16))) SplitLds<D, RT> lds;
+    const Request s = request_of(a, blockIdx.y);
+    const int rb = (int)blockIdx.x / a.kv_heads;
+    Piece p = {s, (int)blockIdx.y, (int)blockIdx.x - rb * a.kv_heads, rb * 16 * RT, s.lo, s.hi, nullptr};
+    if (p.row0 < s.rows)
+        split_piece<D, RT, DT, LAYOUT>(a, p, lds);
+}
+
+// The tiles of all units in a row, cut into equal ranges, split_groups a CU:
+// every workgroup streams the same number of keys, whatever the lengths of
+// the requests and however far the host's bound is above them.  A unit that lies
+// in one range is written out; the others' pieces (a range has two at most:
+// where it begins and where it ends) go to the workspace and are joined by a
+// second kernel.
+//
+// Workspace: int32 cost of a range; int32 cost before each request, per unit
+// (requests + 1 of them); from the next multiple of four words on, two pieces a range.
+__device__ __host__ __forceinline__ int64_t parts_offset(int64_t requests) { return (requests + 2 + 3) / 4 * 4; }
+
+template <int D, int RT, int DT, int LAYOUT>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a, int units)
+{
+    constexpr int NW = kWaves, NT = 64 * NW;
+    __shared__ __attribute__((aligned(16))) SplitLds<D, RT> lds;
+    __shared__ int wave_sums[NW];
+    __shared__ Request found; // the request that holds the range's first tile,
+    __shared__ int found_r, found_before; // its number and the cost before it
+    const int lane = __lane_id(), wave = (int)threadIdx.x >> 6;
+    int32_t *head = reinterpret_cast<int32_t *>(a.workspace);
+
+    // Cost before each request of a batch of NT; `sum` grows by the batch's.
+    auto scan = [&](int cost, int &sum) {
+        int upto = cost;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(upto, d);
+            upto += lane >= d ? up : 0;
+        }
+        if (lane == 63)
+            wave_sums[wave] = upto;
+        __syncthreads();
+        int before = sum + upto - cost;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            before += w < wave ? wave_sums[w] : 0;
+            sum += wave_sums[w];
+        }
+        return before;
+    };
+    auto batch = [&](int r) {
+        Request s = request_of(a, r < a.requests ? r : a.requests - 1);
+        s.cost = r < a.requests ? s.cost : 0;
+        return s;
+    };
+
+    int total = 0, before = 0;
+    Request mine;
+    for (int base = 0; base < a.requests; base += NT) {
+        if (base)
+            __syncthreads(); // wave_sums has been read
+        const int r = base + (int)threadIdx.x;
+        mine = batch(r);
+        before = scan(mine.cost, total);
+        if (blockIdx.x == 0 && r < a.requests)
+            head[1 + r] = before;
+    }
+    const int all = total * units;
+    int per = (all + (int)gridDim.x - 1) / (int)gridDim.x;
+    per = per < kMinRange ? kMinRange : per;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        head[0] = per;
+        head[1 + a.requests] = total;
+    }
+    Range range;
+    range.begin = range.at = (int)blockIdx.x * per;
+    if (range.at >= all)
+        return;
+    range.stop = all - range.at < per ? all : range.at + per;
+    range.parts = a.workspace + parts_offset(a.requests) + (int64_t)blockIdx.x * 2 * piece_floats(D, RT);
+    const int first = range.at / units;
+    int sum = 0;
+    for (int base = 0; base < a.requests; base += NT) {
+        const int r = base + (int)threadIdx.x;
+        if (a.requests > NT) { // once more, batch by batch
+            __syncthreads();
+            mine = batch(r);
+            before = scan(mine.cost, sum);
+        }
+        if (before <= first && first < before + mine.cost) {
+            found = mine;
+            found_r = r;
+            found_before = before;
+        }
+        if (first < sum)
+            break;
+    }
+    __syncthreads();
+    range.r = __builtin_amdgcn_readfirstlane(found_r);
+    range.before = __builtin_amdgcn_readfirstlane(found_before);
+    range.s.t0 = __builtin_amdgcn_readfirstlane(found.t0);
+    range.s.past = __builtin_amdgcn_readfirstlane(found.past);
+    range.s.ctx = __builtin_amdgcn_readfirstlane(found.ctx);
+    range.s.rows = __builtin_amdgcn_readfirstlane(found.rows);
+    range.s.lo = __builtin_amdgcn_readfirstlane(found.lo);
+    range.s.hi = __builtin_amdgcn_readfirstlane(found.hi);
+    range.s.cost = __builtin_amdgcn_readfirstlane(found.cost);
+    Piece p;
+    while (range.template next<D, RT>(a, units, p))
+        split_piece<D, RT, DT, LAYOUT>(a, p, lds);
+}
+
+// Joins the pieces of a row: one workgroup a row, its four waves over the
+// pieces, their lanes over the channels.
 template <int D, int RT, int DT>
-__global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int chunk, int chunks, int row_blocks)
+__global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int units)
 {
     constexpr int E = D / 64;
-    const int lane = __lane_id(), wave = (int)threadIdx.x >> 6;
-    const int row = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + wave);
-    const int kvh = blockIdx.y, r = blockIdx.z;
-    const int rb = row / (16 * RT);
-    const Span s = span_of(a, r, rb * 16 * RT, 16 * RT);
+    __shared__ float lds[4][64 * E + 2];
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int row = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
+    const int32_t *head = reinterpret_cast<const int32_t *>(a.workspace);
+    const int per = head[0], before = head[1 + r], cost = head[2 + r] - before;
+    const Request s = request_of(a, r);
     if (row >= s.rows)
         return;
-    int valid = (s.hi - s.lo + chunk - 1) / chunk;
-    if (valid <= 1)
+    const int rb = row / (16 * RT), unit = rb * a.kv_heads + kvh;
+    const int at = before * units + unit * cost; // where the unit begins
+    const int first = (at + kUnitCost) / per, last = (at + cost - 1) / per; // the ranges that hold tiles of it
+    if (first == last)
         return; // written by its only workgroup
-    valid = valid < chunks ? valid : chunks;
-    const int64_t unit = (int64_t)r * row_blocks * a.kv_heads + rb * a.kv_heads + kvh;
-    const float *w = a.workspace + (unit * chunks * (16 * RT) + (row - rb * 16 * RT)) * (D + 4);
-    const int64_t step = (int64_t)(16 * RT) * (D + 4);
-    float ref = -INFINITY;
-    for (int c = lane; c < valid; c += 64)
-        ref = fmaxf(ref, w[c * step + D]);
-    ref = wave_max_f32(ref);
-    float l = 0.0f, acc[E];
+    constexpr int64_t piece = piece_floats(D, RT);
+    const float *parts = a.workspace + parts_offset(a.requests) + (row - rb * 16 * RT) * (D + 4);
+    // the unit begins a range, or lies behind the end of another
+    auto part_of = [&](int w) { return parts + ((int64_t)w * 2 + (w == first && at > first * per ? 1 : 0)) * piece; };
+    float m = -INFINITY, l = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         acc[e] = 0.0f;
-    for (int c = 0; c < valid; ++c) {
-        const float *p = w + c * step;
-        const float f = p[D] == ref ? 1.0f : __builtin_amdgcn_exp2f(p[D] - ref);
-        l = fmaf(p[D + 1], f, l);
+#pragma unroll 4
+    for (int w = first + wave; w <= last; w += 4) {
+        const float *p = part_of(w);
+        const float pm = p[D], pl = p[D + 1];
+        float v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            acc[e] = fmaf(p[lane * E + e], f, acc[e]);
+            v[e] = p[lane * E + e];
+        const float next = fmaxf(m, pm);
+        const float fa = m == next ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+        const float fb = pm == next ? 1.0f : __builtin_amdgcn_exp2f(pm - next);
+        m = next;
+        l = l * fa + pl * fb;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = acc[e] * fa + v[e] * fb;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        lds[wave][lane * E + e] = acc[e];
+    if (lane == 0) {
+        lds[wave][64 * E] = m;
+        lds[wave][64 * E + 1] = l;
+    }
+    __syncthreads();
+    if (wave)
+        return;
+    float ref = lds[0][64 * E];
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+        ref = fmaxf(ref, lds[w][64 * E]);
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float mw = lds[w][64 * E];
+        const float f = mw == ref ? 1.0f : __builtin_amdgcn_exp2f(mw - ref);
+        l += lds[w][64 * E + 1] * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] += lds[w][lane * E + e] * f;
     }
     const float n = l == 0.0f ? 0.0f : 1.0f / l;
-    const int i = row / a.group, head = kvh * a.group + row - i * a.group;
-    uint16_t *out = a.out + ((int64_t)(s.t0 + i) * a.q_heads + head) * D + lane * E;
+    const int i = row / a.group, qh = kvh * a.group + row - i * a.group;
+    uint16_t *out = a.out + ((int64_t)(s.t0 + i) * a.q_heads + qh) * D + lane * E;
     if (E == 2)
         *reinterpret_cast<uint32_t *>(out) = Act<DT>::pack(acc[0] * n, acc[E - 1] * n);
     else
@@ -409,54 +628,58 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int chu
 }
 
 struct SplitShape {
-    int rt, row_blocks, chunk, chunks;
+    int rt, units;
+    int groups; // workgroups of the streamed form; 0: one a unit
 };
 
-SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_context,
+SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t max_new, int64_t max_context,
                        int64_t window)
 {
     SplitShape p;
     const int64_t rows = max_new * group;
     p.rt = rows <= 16 ? 1 : 2;
-    p.row_blocks = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+    p.units = (int)((rows + 16 * p.rt - 1) / (16 * p.rt) * kv_heads);
     int64_t span = max_context;
     if (window && window + max_new + kTile < span)
         span = window + max_new + kTile;
-    const int64_t units = requests * kv_heads * p.row_blocks;
-    const int64_t want = (1536 + units - 1) / units;
-    const int64_t step = 4 * kTile;
-    int64_t chunk = ((span + want - 1) / want + step - 1) / step * step;
-    if (span <= 512)
-        chunk = 512;
-    p.chunk = (int)(chunk < step ? step : chunk);
-    p.chunks = (int)((span + p.chunk - 1) / p.chunk);
-    if (p.chunks < 1)
-        p.chunks = 1;
+    const int64_t tiles = (span + kTile - 1) / kTile, all = (tiles + kUnitCost) * requests * p.units;
+    p.groups = device_cu_count() * split_groups((int)head_dim, p.rt);
+    if (tiles <= 8 || all >= (int64_t(1) << 31) - (1 << 20) || requests * p.units >= 4 * (int64_t)p.groups)
+        p.groups = 0;
+    else if (all < kMinRange * (int64_t)p.groups)
+        p.groups = (int)((all + kMinRange - 1) / kMinRange);
     return p;
 }
 
-template <int D, int RT, int DT>
+template <int D, int RT, int DT, int LAYOUT>
 hipError_t launch_split(const KvAttnArgs &a, const SplitShape &p, hipStream_t stream)
 {
-    const dim3 grid((unsigned)p.chunks, (unsigned)(p.row_blocks * a.kv_heads), (unsigned)a.requests);
-    if (a.block_shift >= 6)
-        kv_split_kernel<D, RT, DT, true><<<grid, dim3(kThreads), 0, stream>>>(a, p.chunk, p.chunks);
-    else
-        kv_split_kernel<D, RT, DT, false><<<grid, dim3(kThreads), 0, stream>>>(a, p.chunk, p.chunks);
+    if (p.groups == 0) {
+        kv_unit_kernel<D, RT, DT, LAYOUT><<<dim3((unsigned)p.units, (unsigned)a.requests), dim3(64 * kWaves), 0, stream>>>(a, p.units);
+        return hipGetLastError();
+    }
+    kv_stream_kernel<D, RT, DT, LAYOUT><<<dim3((unsigned)p.groups), dim3(64 * kWaves), 0, stream>>>(a, p.units);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.chunks == 1)
+    if (e != hipSuccess)
         return e;
-    const int rows = a.max_new * a.group;
-    kv_join_kernel<D, RT, DT><<<dim3((unsigned)((rows + 3) / 4), (unsigned)a.kv_heads, (unsigned)a.requests),
-                                dim3(kThreads), 0, stream>>>(a, p.chunk, p.chunks, p.row_blocks);
+    kv_join_kernel<D, RT, DT><<<dim3((unsigned)(a.max_new * a.group), (unsigned)a.kv_heads, (unsigned)a.requests),
+                                dim3(kThreads), 0, stream>>>(a, p.units);
     return hipGetLastError();
+}
+
+template <int D, int RT, int DT>
+hipError_t launch_layout(const KvAttnArgs &a, const SplitShape &p, hipStream_t stream)
+{
+    if (a.block_shift < 6)
+        return launch_split<D, RT, DT, kNarrow>(a, p, stream);
+    return a.block_shift == 6 ? launch_split<D, RT, DT, kWhole>(a, p, stream) : launch_split<D, RT, DT, kHalf>(a, p, stream);
 }
 
 template <int D, int DT>
 hipError_t launch_dim(const KvAttnArgs &a, hipStream_t stream)
 {
-    const SplitShape p = split_shape(a.requests, a.kv_heads, a.group, a.max_new, a.max_context, a.window);
-    return p.rt == 1 ? launch_split<D, 1, DT>(a, p, stream) : launch_split<D, 2, DT>(a, p, stream);
+    const SplitShape p = split_shape(a.requests, a.kv_heads, D, a.group, a.max_new, a.max_context, a.window);
+    return p.rt == 1 ? launch_layout<D, 1, DT>(a, p, stream) : launch_layout<D, 2, DT>(a, p, stream);
 }
 
 } // namespace
@@ -464,10 +687,10 @@ hipError_t launch_dim(const KvAttnArgs &a, hipStream_t stream)
 int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                int64_t requests, int64_t max_new, int64_t max_context, int64_t window)
 {
-    const SplitShape p = split_shape(requests, kv_heads, q_heads / kv_heads, max_new, max_context, window);
-    if (p.chunks == 1)
+    const SplitShape p = split_shape(requests, kv_heads, head_dim, q_heads / kv_heads, max_new, max_context, window);
+    if (p.groups == 0)
         return 0;
-    return requests * kv_heads * p.row_blocks * p.chunks * (16 * p.rt) * (head_dim + 4) * (int64_t)sizeof(float);
+    return (parts_offset(requests) + (int64_t)p.groups * 2 * piece_floats((int)head_dim, p.rt)) * (int64_t)sizeof(float);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, int dtype, hipStream_t stream)

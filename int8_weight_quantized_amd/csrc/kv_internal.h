@@ -82,6 +82,8 @@ struct KvAttnArgs {
     int32_t causal, window;
     float *workspace;
 };
+int device_cu_count(); // qw_api.hip
+
 // Workspace bytes of the shape's split along the context (0: none).
 int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                int64_t requests, int64_t max_new, int64_t max_context, int64_t window);
