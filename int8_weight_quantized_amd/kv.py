@@ -18,6 +18,8 @@ import ctypes
 import math
 from typing import NamedTuple
 
+import int8_weight_quantized_amd as _pkg  # (partly initialised here; its attributes are looked up when a call needs them)
+
 KV_HEAD_DIMS = (64, 128)
 KV_BLOCK_SIZES = (16, 32, 64, 128)
 KV_PLAN_MAX_REQUESTS = 8191
@@ -56,20 +58,32 @@ def _declare(lib):
     lib.qw_kv_attention_workspace.restype = i64
 
 
-def _base():
-    import int8_weight_quantized_amd as base
-    return base
+# The calls below are a few microseconds of kernel each in decode, so their
+# own time counts.  Each first tests its arguments with plain attribute
+# reads; only where that fails do the _validate_* helpers run, which say what
+# is wrong (and let pass what the quick test was too narrow for).
+
+_torch = None
+_raw_stream = None
 
 
-_dtype_codes = None
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _torch = torch
+    _codes.update({torch.float16: 0, torch.bfloat16: 1})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:
+        _raw_stream = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
+    return torch
+
+
+_codes = {}  # torch dtype -> qw_dtype; filled with torch
 
 
 def _dtype_code(dtype, name):
-    global _dtype_codes
-    if _dtype_codes is None:
-        import torch
-        _dtype_codes = {torch.float16: 0, torch.bfloat16: 1}
-    code = _dtype_codes.get(dtype)
+    _torch or _load_torch()
+    code = _codes.get(dtype)
     if code is None:
         raise TypeError("%s must be torch.float16 or torch.bfloat16, got %s" % (name, dtype))
     return code
@@ -105,7 +119,7 @@ def _heads(t, name, device, heads=None, dim=None, tokens=None, dtype=None):
 
 def _validate_cache(k_cache, v_cache, k_scales, v_scales, device, heads=None, dim=None):
     import torch
-    check = _base()._check
+    check = _pkg._check
     check(k_cache, "k_cache", torch.int8, ndim=4, device=device)
     blocks, h, size, d = k_cache.shape
     if size not in KV_BLOCK_SIZES:
@@ -122,14 +136,14 @@ def _validate_cache(k_cache, v_cache, k_scales, v_scales, device, heads=None, di
 
 def _validate_ints(device, **named):
     import torch
-    check = _base()._check
+    check = _pkg._check
     for name, (t, shape) in named.items():
         check(t, name, torch.int32, shape=shape, device=device)
 
 
 def _raise(status, where):
     if status:
-        raise _base().QwError(status, where)
+        raise _pkg.QwError(status, where)
 
 
 def kv_cache(num_blocks: int, kv_heads: int, head_dim: int, block_size: int = 64, device="cuda") -> KvCache:
@@ -149,7 +163,7 @@ def kv_cache(num_blocks: int, kv_heads: int, head_dim: int, block_size: int = 64
 
 def _validate_plan(past, fresh, block_table, free_blocks, block_size, max_tokens, device):
     import torch
-    check = _base()._check
+    check = _pkg._check
     check(past, "past", torch.int32, ndim=1, device=device)
     requests = past.shape[0]
     check(fresh, "fresh", torch.int32, shape=(requests,), device=device)
@@ -171,27 +185,42 @@ def kv_plan(past, fresh, block_table, free_blocks, block_size: int, max_tokens: 
     (int32 [R]) and adds fresh[r]; new blocks are taken from free_blocks
     (int32) in order and entered into block_table (int32 [R, W], in place).
     max_tokens sizes the token arrays (their padding is -1)."""
-    base = _base()
-    import torch
-    device = base._require_gpu(past, "past")
-    requests = _validate_plan(past, fresh, block_table, free_blocks, block_size, max_tokens, device)
+    torch = _torch or _load_torch()
+    i32 = torch.int32
+    try:
+        index = past.get_device()
+        requests, = past.shape
+        rows, width = block_table.shape
+        n_free, = free_blocks.shape
+        fine = (index >= 0 and past.dtype is i32 and fresh.dtype is i32 and block_table.dtype is i32 and free_blocks.dtype is i32
+                and fresh.shape == past.shape and rows == requests and past.is_contiguous() and fresh.is_contiguous()
+                and block_table.is_contiguous() and free_blocks.is_contiguous() and fresh.get_device() == index
+                and block_table.get_device() == index and free_blocks.get_device() == index and block_size in KV_BLOCK_SIZES
+                and max_tokens >= 0 and requests <= KV_PLAN_MAX_REQUESTS)
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        device = _pkg._require_gpu(past, "past")
+        requests = _validate_plan(past, fresh, block_table, free_blocks, block_size, max_tokens, device)
+        index, width, n_free = past.get_device(), block_table.shape[1], free_blocks.shape[0]
     # one allocation for the five arrays
-    buf = torch.empty(2 * requests + 3 + 2 * max_tokens, dtype=torch.int32, device=device)
-    cu, context, counts, positions, slots = buf.split((requests + 1, requests, 2, max_tokens, max_tokens))
+    buf = torch.empty(2 * requests + 3 + 2 * max_tokens, dtype=i32, device=past.device)
+    cu, context, counts, positions, slots = buf.split_with_sizes((requests + 1, requests, 2, max_tokens, max_tokens))
     p = buf.data_ptr()
     p_ctx = p + 4 * (requests + 1)
     p_counts = p_ctx + 4 * requests
     p_pos = p_counts + 8
-    _raise(base.library().qw_kv_plan(past.data_ptr(), fresh.data_ptr(), requests, block_table.data_ptr(),
-                                     block_table.shape[1], free_blocks.data_ptr(), free_blocks.shape[0], block_size,
-                                     max_tokens, p, p_ctx, p_pos, p_pos + 4 * max_tokens, p_counts,
-                                     base._stream_of(past)), "qw_kv_plan")
+    status = _pkg.library().qw_kv_plan(past.data_ptr(), fresh.data_ptr(), requests, block_table.data_ptr(), width,
+                                       free_blocks.data_ptr(), n_free, block_size, max_tokens, p, p_ctx, p_pos,
+                                       p_pos + 4 * max_tokens, p_counts, _raw_stream(index))
+    if status:
+        _raise(status, "qw_kv_plan")
     return KvPlan(block_table, cu, context, positions, slots, counts)
 
 
 def _validate_norm_rope(q, k, positions, cos, sin, q_weight, k_weight, out, device):
     import torch
-    check = _base()._check
+    check = _pkg._check
     code = _dtype_code(q.dtype, "q")
     sq = _heads(q, "q", device)
     tokens, hq, dim = q.shape
@@ -225,16 +254,61 @@ def qk_norm_rope(q, k, positions, cos, sin, q_weight=None, k_weight=None, eps: f
     bf16 (strided token views allowed), positions int32 [T], cos and sin fp32
     [P, rot_dim / 2].  ``interleaved`` rotates pairs (2 i, 2 i + 1), else
     (i, i + rot_dim / 2).  Returns (q, k); ``out=(q, k)`` rotates in place."""
-    base = _base()
-    device = base._require_gpu(q, "q")
-    code, tokens, hq, hk, dim, rot, sq, sk, qo, sqo, ko, sko = _validate_norm_rope(
-        q, k, positions, cos, sin, q_weight, k_weight, out, device)
-    _raise(base.library().qw_qk_norm_rope(
+    torch = _torch or _load_torch()
+    try:
+        index = q.get_device()
+        dtype = q.dtype
+        code = _codes[dtype]
+        tokens, hq, dim = q.shape
+        hk = k.shape[1]
+        span, half = cos.shape
+        rot = 2 * half
+        sq, sk = q.stride(), k.stride()
+        fine = (out is None and index >= 0 and sq[0] >= hq * dim and sk[0] >= hk * dim and dim in KV_HEAD_DIMS and k.shape == (tokens, hk, dim)
+                and k.dtype is dtype and sq[2] == 1 and sk[2] == 1 and sq[1] == dim and sk[1] == dim and sq[0] % 8 == 0
+                and sk[0] % 8 == 0 and hq > 0 and hk > 0 and k.get_device() == index
+                and positions.dtype is torch.int32 and positions.shape == (tokens,) and positions.is_contiguous()
+                and positions.get_device() == index and cos.dtype is torch.float32 and sin.dtype is torch.float32
+                and sin.shape == cos.shape and cos.is_contiguous() and sin.is_contiguous() and cos.get_device() == index
+                and sin.get_device() == index and rot <= dim and rot % 16 == 0)
+        if fine and q_weight is not None:
+            fine = (q_weight.dtype is dtype and k_weight.dtype is dtype and q_weight.shape == (dim,) and k_weight.shape == (dim,)
+                    and q_weight.is_contiguous() and k_weight.is_contiguous() and q_weight.get_device() == index
+                    and k_weight.get_device() == index)
+        elif fine:
+            fine = k_weight is None
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if fine:
+        sq, sk, sqo, sko = sq[0], sk[0], hq * dim, hk * dim
+        qo = torch.empty((tokens, hq, dim), dtype=dtype, device=q.device)
+        ko = torch.empty((tokens, hk, dim), dtype=dtype, device=q.device)
+    else:
+        device = _pkg._require_gpu(q, "q")
+        code, tokens, hq, hk, dim, rot, sq, sk, qo, sqo, ko, sko = _validate_norm_rope(
+            q, k, positions, cos, sin, q_weight, k_weight, out, device)
+        index, span = q.get_device(), cos.shape[0]
+    status = _pkg.library().qw_qk_norm_rope(
         q.data_ptr(), sq, k.data_ptr(), sk, code, tokens, hq, hk, dim, positions.data_ptr(), cos.data_ptr(), sin.data_ptr(),
-        cos.shape[0], rot, 1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
-        None if k_weight is None else k_weight.data_ptr(), eps, qo.data_ptr(), sqo, ko.data_ptr(), sko,
-        base._stream_of(q)), "qw_qk_norm_rope")
+        span, rot, 1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
+        None if k_weight is None else k_weight.data_ptr(), eps, qo.data_ptr(), sqo, ko.data_ptr(), sko, _raw_stream(index))
+    if status:
+        _raise(status, "qw_qk_norm_rope")
     return qo, ko
+
+
+def _cache_fits(k_cache, v_cache, k_scales, v_scales, index):
+    """Whether the four tensors are a cache on device `index` (the quick test
+    of _validate_cache)."""
+    torch = _torch
+    blocks, heads, size, dim = k_cache.shape
+    return (dim in KV_HEAD_DIMS and size in KV_BLOCK_SIZES and blocks > 0 and heads > 0
+            and k_cache.dtype is torch.int8 and v_cache.dtype is torch.int8 and k_scales.dtype is torch.float32
+            and v_scales.dtype is torch.float32 and v_cache.shape == (blocks, heads, dim, size)
+            and k_scales.shape == (blocks, heads) and v_scales.shape == (blocks, heads) and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous()
+            and k_cache.get_device() == index and v_cache.get_device() == index and k_scales.get_device() == index
+            and v_scales.get_device() == index)
 
 
 def _validate_write(k, v, slots, cache, device):
@@ -244,7 +318,7 @@ def _validate_write(k, v, slots, cache, device):
     tokens, heads, dim = k.shape
     sv = _heads(v, "v", device, heads=heads, dim=dim, tokens=tokens, dtype=k.dtype)
     blocks, _, size, _ = _validate_cache(*cache, device, heads=heads, dim=dim)
-    _base()._check(slots, "slots", torch.int32, shape=(tokens,), device=device)
+    _pkg._check(slots, "slots", torch.int32, shape=(tokens,), device=device)
     return code, tokens, heads, dim, sk, sv, blocks, size
 
 
@@ -253,18 +327,37 @@ def kv_write(k, v, slots, k_cache, v_cache, k_scales, v_scales) -> None:
     views allowed) into the cache at slots (int32 [T]; -1 skips a token).
     The tokens of a block follow each other in one call, as kv_plan numbers
     them; a block's scale grows to the largest value it holds."""
-    base = _base()
-    device = base._require_gpu(k, "k")
-    code, tokens, heads, dim, sk, sv, blocks, size = _validate_write(k, v, slots, (k_cache, v_cache, k_scales, v_scales), device)
-    _raise(base.library().qw_kv_write(
+    torch = _torch or _load_torch()
+    try:
+        index = k.get_device()
+        dtype = k.dtype
+        code = _codes[dtype]
+        tokens, heads, dim = k.shape
+        blocks, cache_heads, size, cache_dim = k_cache.shape
+        sk, sv = k.stride(), v.stride()
+        fine = (index >= 0 and sk[0] >= heads * dim and sv[0] >= heads * dim and v.shape == k.shape and v.dtype is dtype and sk[2] == 1 and sv[2] == 1
+                and sk[1] == dim and sv[1] == dim and sk[0] % 8 == 0 and sv[0] % 8 == 0 and v.get_device() == index
+                and slots.dtype is torch.int32 and slots.shape == (tokens,) and slots.is_contiguous()
+                and slots.get_device() == index and cache_heads == heads and cache_dim == dim
+                and _cache_fits(k_cache, v_cache, k_scales, v_scales, index))
+        sk, sv = sk[0], sv[0]
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        device = _pkg._require_gpu(k, "k")
+        code, tokens, heads, dim, sk, sv, blocks, size = _validate_write(k, v, slots, (k_cache, v_cache, k_scales, v_scales), device)
+        index = k.get_device()
+    status = _pkg.library().qw_kv_write(
         k.data_ptr(), sk, v.data_ptr(), sv, code, tokens, heads, dim, slots.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), blocks, size, base._stream_of(k)), "qw_kv_write")
+        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), blocks, size, _raw_stream(index))
+    if status:
+        _raise(status, "qw_kv_write")
 
 
 def _validate_read(slots, cache, dtype, device):
     import torch
     code = _dtype_code(dtype, "dtype")
-    _base()._check(slots, "slots", torch.int32, ndim=1, device=device)
+    _pkg._check(slots, "slots", torch.int32, ndim=1, device=device)
     blocks, heads, size, dim = _validate_cache(*cache, device)
     return code, slots.shape[0], blocks, heads, size, dim
 
@@ -272,22 +365,34 @@ def _validate_read(slots, cache, dtype, device):
 def kv_read(slots, k_cache, v_cache, k_scales, v_scales, dtype=None):
     """The keys and values that slots (int32 [T]) of the cache stand for, in
     fp16 (or the given 16-bit dtype): (k, v), each [T, H, D]; zeros for -1."""
-    import torch
-    base = _base()
-    device = base._require_gpu(slots, "slots")
+    torch = _torch or _load_torch()
     dtype = torch.float16 if dtype is None else dtype
-    code, tokens, blocks, heads, size, dim = _validate_read(slots, (k_cache, v_cache, k_scales, v_scales), dtype, device)
-    k = torch.empty((tokens, heads, dim), dtype=dtype, device=device)
-    v = torch.empty((tokens, heads, dim), dtype=dtype, device=device)
-    _raise(base.library().qw_kv_read(
+    try:
+        index = slots.get_device()
+        code = _codes[dtype]
+        tokens, = slots.shape
+        blocks, heads, size, dim = k_cache.shape
+        fine = (index >= 0 and slots.dtype is torch.int32 and slots.is_contiguous()
+                and _cache_fits(k_cache, v_cache, k_scales, v_scales, index))
+    except (AttributeError, KeyError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        device = _pkg._require_gpu(slots, "slots")
+        code, tokens, blocks, heads, size, dim = _validate_read(slots, (k_cache, v_cache, k_scales, v_scales), dtype, device)
+        index = slots.get_device()
+    k = torch.empty((tokens, heads, dim), dtype=dtype, device=slots.device)
+    v = torch.empty_like(k)
+    status = _pkg.library().qw_kv_read(
         slots.data_ptr(), tokens, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), blocks,
-        size, heads, dim, code, k.data_ptr(), v.data_ptr(), base._stream_of(slots)), "qw_kv_read")
+        size, heads, dim, code, k.data_ptr(), v.data_ptr(), _raw_stream(index))
+    if status:
+        _raise(status, "qw_kv_read")
     return k, v
 
 
 def _validate_attention(q, cache, block_table, context, cu_tokens, max_new, max_context, scale, window, out, device):
     import torch
-    check = _base()._check
+    check = _pkg._check
     code = _dtype_code(q.dtype, "q")
     sq = _heads(q, "q", device)
     tokens, heads, dim = q.shape
@@ -318,7 +423,7 @@ def kv_attention_workspace(q, k_cache, block_table, max_new: int, max_context=No
     tokens, heads, dim = q.shape
     requests, width = block_table.shape
     size = k_cache.shape[2]
-    n = int(_base().library().qw_kv_attention_workspace(
+    n = int(_pkg.library().qw_kv_attention_workspace(
         tokens, heads, k_cache.shape[1], dim, size, width, requests, max_new,
         width * size if max_context is None else max_context, window))
     if n < 0:
@@ -337,23 +442,52 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
     lets a query see that many keys, its own the last.  Rows that see
     nothing are zero.  ``workspace`` (uint8, kv_attention_workspace bytes) is
     allocated when not given.  Returns [T, Hq, D]."""
-    import torch
-    base = _base()
-    device = base._require_gpu(q, "q")
-    code, tokens, heads, dim, sq, blocks, kv_heads, size, requests, width, max_context, scale, out = _validate_attention(
-        q, (k_cache, v_cache, k_scales, v_scales), block_table, context, cu_tokens, max_new, max_context, scale, window, out,
-        device)
-    lib = base.library()
+    torch = _torch or _load_torch()
+    try:
+        index = q.get_device()
+        dtype = q.dtype
+        code = _codes[dtype]
+        tokens, heads, dim = q.shape
+        blocks, kv_heads, size, cache_dim = k_cache.shape
+        requests, width = block_table.shape
+        sq = q.stride()
+        i32 = torch.int32
+        fine = (out is None and index >= 0 and tokens > 0 and sq[2] == 1 and sq[1] == dim and sq[0] % 8 == 0
+                and sq[0] >= heads * dim and cache_dim == dim and heads % kv_heads == 0 and block_table.dtype is i32
+                and context.dtype is i32 and cu_tokens.dtype is i32 and context.shape == (requests,)
+                and cu_tokens.shape == (requests + 1,) and block_table.is_contiguous() and context.is_contiguous()
+                and cu_tokens.is_contiguous() and block_table.get_device() == index and context.get_device() == index
+                and cu_tokens.get_device() == index and max_new >= 0 and window >= 0
+                and _cache_fits(k_cache, v_cache, k_scales, v_scales, index))
+        sq = sq[0]
+        if max_context is None:
+            max_context = width * size
+        fine = fine and max_context >= 0
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError, ZeroDivisionError):
+        fine = False
+    if fine:
+        if scale is None:
+            scale = 1.0 / math.sqrt(dim)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
+    else:
+        device = _pkg._require_gpu(q, "q")
+        code, tokens, heads, dim, sq, blocks, kv_heads, size, requests, width, max_context, scale, out = _validate_attention(
+            q, (k_cache, v_cache, k_scales, v_scales), block_table, context, cu_tokens, max_new, max_context, scale, window, out,
+            device)
+        index = q.get_device()
+    lib = _pkg.library()
     if workspace is None:
         need = lib.qw_kv_attention_workspace(tokens, heads, kv_heads, dim, size, width, requests, max_new, max_context, window)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
-        base._check(workspace, "workspace", torch.uint8, ndim=1, device=device)
-    _raise(lib.qw_kv_attention(
+        _pkg._check(workspace, "workspace", torch.uint8, ndim=1, device=q.device)
+        need = workspace.numel()
+    status = lib.qw_kv_attention(
         q.data_ptr(), sq, code, tokens, heads, kv_heads, dim, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
         v_scales.data_ptr(), blocks, size, block_table.data_ptr(), width, context.data_ptr(), cu_tokens.data_ptr(), requests,
         max_new, max_context, scale, 1 if causal else 0, window, out.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        base._stream_of(q)), "qw_kv_attention")
+        None if workspace is None else workspace.data_ptr(), need if need > 0 else 0, _raw_stream(index))
+    if status:
+        _raise(status, "qw_kv_attention")
     return out
