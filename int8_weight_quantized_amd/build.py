@@ -48,6 +48,7 @@ UNITS = {
     "qk_norm_rope.hip": [],
     "kv_cache.hip": ["-ffp-contract=off"],
     "kv_attention.hip": [],
+    "kv_prompt.hip": [],
 }
 
 

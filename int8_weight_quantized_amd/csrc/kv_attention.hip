@@ -25,8 +25,7 @@
 // Query rows that share a key head (the heads of its group, for each new
 // token) form the columns of one matrix product, so the cache is read once
 // for all of them.
-#include "kv_device.h"
-#include "kv_internal.h"
+#include "kv_attention_device.h"
 
 namespace qw {
 
@@ -59,60 +58,24 @@ enum Layout {
     kHalf = 2    // in one block of 128: a value row of the tile is half a cache line
 };
 
-__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
-
-// What one request asks for.
-struct Request {
-    int t0, past; // first token; cached tokens before it (negative where there are more queries than cached tokens)
-    int ctx;      // cached tokens
-    int rows;     // query rows of a key head: those of at most max_new tokens
-    int lo, hi;   // keys that any of the rows sees; lo is a multiple of kTile
-    int cost;     // kTile-key tiles of that range, at least one, and kUnitCost; 0 without rows
+// A request, with the keys that any of its rows sees and their cost.
+struct Request : KvRequest {
+    int lo, hi; // keys; lo is a multiple of kTile
+    int cost;   // kTile-key tiles of that range, at least one, and kUnitCost; 0 without rows
 };
 
 __device__ __forceinline__ Request request_of(const KvAttnArgs &a, int r)
 {
     Request s;
-    s.t0 = clampi(a.cu_tokens[r], 0, a.tokens);
-    const int n = clampi(a.cu_tokens[r + 1], s.t0, a.tokens) - s.t0;
-    const int queries = n < a.max_new ? n : a.max_new;
-    s.ctx = clampi(a.context[r], 0, a.max_context);
-    s.past = s.ctx - n;
-    s.rows = queries * a.group;
+    static_cast<KvRequest &>(s) = kv_request(a, r);
     s.lo = s.hi = 0;
     s.cost = 0;
-    if (queries) {
-        s.hi = a.causal ? clampi(s.past + queries, 0, s.ctx) : s.ctx;
-        s.lo = a.window ? clampi(s.past - a.window + 1, 0, s.hi) & ~(kTile - 1) : 0;
+    if (s.rows) {
+        s.hi = a.causal ? kv_clamp(s.past + s.rows / a.group, 0, s.ctx) : s.ctx;
+        s.lo = a.window ? kv_clamp(s.past - a.window + 1, 0, s.hi) & ~(kTile - 1) : 0;
         s.cost = (s.hi > s.lo ? (s.hi - s.lo + kTile - 1) / kTile : 1) + kUnitCost;
     }
     return s;
-}
-
-// 8 activations -> fp16 (bf16 after multiplication by `up`, a power of two).
-template <int DT>
-__device__ __forceinline__ half8_t to_half8(u32x4_t v, float up)
-{
-    if (DT == QW_F16)
-        return __builtin_bit_cast(half8_t, v);
-    float f[8];
-    unpack8<DT>(v, f);
-    half8_t h;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        h[i] = (_Float16)(f[i] * up);
-    return h;
-}
-
-// The power of two that brings a bf16 row's largest magnitude to
-// [2^14, 2^15), and its inverse; 1 for rows that are zero or not finite.
-__device__ __forceinline__ void row_power(float top, float &up, float &down)
-{
-    const uint32_t e = __builtin_bit_cast(uint32_t, top) >> 23 & 0xffu; // top >= 0
-    const int p = clampi(127 + 14 - (int)e, -113, 100);
-    const bool plain = e == 0 || e == 255;
-    up = plain ? 1.0f : __builtin_bit_cast(float, (uint32_t)(127 + p) << 23);
-    down = plain ? 1.0f : __builtin_bit_cast(float, (uint32_t)(127 - p) << 23);
 }
 
 // ---------------------------------------------------------------------------
@@ -229,13 +192,13 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
             }
         float up = 1.0f, down = 1.0f;
         if (DT == QW_BF16)
-            row_power(max_xor32(max_xor16(top)), up, down);
+            kv_row_power(max_xor32(max_xor16(top)), up, down);
         mult[t] = a.scale_log2 * down;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                q[t][c][h] = to_half8<DT>(raw[c][h], up);
+                q[t][c][h] = kv_half8<DT>(raw[c][h], up);
         lim_hi[t] = in ? (a.causal ? p.s.past + i + 1 : p.s.ctx) : 0;
         lim_lo[t] = a.window ? p.s.past + i - a.window + 1 : 0;
     }
@@ -627,6 +590,11 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int uni
         *out = (uint16_t)Act<DT>::pack(acc[0] * n, 0.0f);
 }
 
+bool prompt_preferred(int64_t requests, int64_t kv_heads, int64_t group, int64_t max_new)
+{
+    return max_new * group > 32;
+}
+
 struct SplitShape {
     int rt, units;
     int groups; // workgroups of the streamed form; 0: one a unit
@@ -687,6 +655,8 @@ hipError_t launch_dim(const KvAttnArgs &a, hipStream_t stream)
 int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                int64_t requests, int64_t max_new, int64_t max_context, int64_t window)
 {
+    if (prompt_preferred(requests, kv_heads, q_heads / kv_heads, max_new))
+        return 0;
     const SplitShape p = split_shape(requests, kv_heads, head_dim, q_heads / kv_heads, max_new, max_context, window);
     if (p.groups == 0)
         return 0;
@@ -695,6 +665,8 @@ int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, int dtype, hipStream_t stream)
 {
+    if (prompt_preferred(a.requests, a.kv_heads, a.group, a.max_new))
+        return launch_kv_prompt(a, dtype, stream);
     if (a.head_dim == 64)
         return dtype == QW_F16 ? launch_dim<64, QW_F16>(a, stream) : launch_dim<64, QW_BF16>(a, stream);
     if (a.head_dim == 128)

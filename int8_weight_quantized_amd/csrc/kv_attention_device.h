@@ -1,0 +1,57 @@
+// kv_attention_device.h -- what the attention kernels over the paged KV cache
+// share: a request's sizes as the device holds them, and query rows as fp16
+// operands.
+#pragma once
+
+#include "kv_device.h"
+#include "kv_internal.h"
+
+namespace qw {
+
+__device__ __forceinline__ int kv_clamp(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// What one request asks for, bounded by what the arguments describe.
+struct KvRequest {
+    int t0, past; // first token; cached tokens before it (negative where there are more queries than cached tokens)
+    int ctx;      // cached tokens
+    int rows;     // query rows of a key head: those of at most max_new tokens
+};
+
+__device__ __forceinline__ KvRequest kv_request(const KvAttnArgs &a, int r)
+{
+    KvRequest s;
+    s.t0 = kv_clamp(a.cu_tokens[r], 0, a.tokens);
+    const int n = kv_clamp(a.cu_tokens[r + 1], s.t0, a.tokens) - s.t0;
+    s.ctx = kv_clamp(a.context[r], 0, a.max_context);
+    s.past = s.ctx - n;
+    s.rows = (n < a.max_new ? n : a.max_new) * a.group;
+    return s;
+}
+
+// 8 activations -> fp16 (bf16 after multiplication by `up`, a power of two).
+template <int DT>
+__device__ __forceinline__ half8_t kv_half8(u32x4_t v, float up)
+{
+    if (DT == QW_F16)
+        return __builtin_bit_cast(half8_t, v);
+    float f[8];
+    unpack8<DT>(v, f);
+    half8_t h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        h[i] = (_Float16)(f[i] * up);
+    return h;
+}
+
+// The power of two that brings a bf16 row's largest magnitude to
+// [2^14, 2^15), and its inverse; 1 for rows that are zero or not finite.
+__device__ __forceinline__ void kv_row_power(float top, float &up, float &down)
+{
+    const uint32_t e = __builtin_bit_cast(uint32_t, top) >> 23 & 0xffu; // top >= 0
+    const int p = kv_clamp(127 + 14 - (int)e, -113, 100);
+    const bool plain = e == 0 || e == 255;
+    up = plain ? 1.0f : __builtin_bit_cast(float, (uint32_t)(127 + p) << 23);
+    down = plain ? 1.0f : __builtin_bit_cast(float, (uint32_t)(127 - p) << 23);
+}
+
+} // namespace qw
