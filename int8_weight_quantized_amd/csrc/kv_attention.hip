@@ -91,8 +91,10 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs &a, int r)
 // then one contiguous 16-byte load a lane from the transposed values.
 // Nothing passes through LDS or between lanes but the row maximum.
 //
-// Bound by HBM: 2 * D + 8 / B bytes a key and head, each read once, straight
-// into registers, past the caches (6.0 against 5.6 TB/s on long contexts).  A
+// Bound by HBM: 2 * D + 8 / B bytes a key and head, read straight into
+// registers; past the caches where there is one block of query rows (ONCE:
+// 6.0 against 5.6 TB/s on long contexts), else through them (up to a fifth
+// faster: 898 -> 718 us for eight chunks of up to 512 tokens).  A
 // tile is D / 4 loads of 16 bytes a lane in flight; asking for the next tile
 // before this one's products gained nothing, with eight waves a CU.
 // ---------------------------------------------------------------------------
@@ -101,6 +103,14 @@ struct SplitLds {
     float o[kWaves][16 * RT][D + 4];
     float m[kWaves][16 * RT], l[kWaves][16 * RT];
 };
+
+// Codes that are read once bypass the caches.
+template <bool ONCE>
+__device__ __forceinline__ u32x4_t load_codes(const int8_t *p)
+{
+    const u32x4_t *at = reinterpret_cast<const u32x4_t *>(p);
+    return ONCE ? __builtin_nontemporal_load(at) : *at;
+}
 
 // Floats of an unfinished piece in the workspace: 16 RT rows of D channels,
 // the reference M, the denominator, and two of padding.
@@ -152,7 +162,7 @@ struct Range {
     }
 };
 
-template <int D, int RT, int DT, int LAYOUT>
+template <int D, int RT, int DT, int LAYOUT, bool ONCE>
 __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p, SplitLds<D, RT> &lds)
 {
     constexpr int CH = D / 64; // 64-channel pieces of a key row
@@ -251,16 +261,11 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                kraw[i][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(kp + i * 4 * D + c * 64));
+                kraw[i][c] = load_codes<ONCE>(kp + i * 4 * D + c * 64);
         const float ks = a.k_scales[vb], vs = a.v_scales[vb];
 #pragma unroll
-        for (int d = 0; d < DTILES; ++d) {
-            // (half a line is not streamed past the caches: the other half follows)
-            if (LAYOUT == kHalf)
-                vraw[d] = *reinterpret_cast<const u32x4_t *>(vp + d * 16 * block);
-            else
-                vraw[d] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(vp + d * 16 * block));
-        }
+        for (int d = 0; d < DTILES; ++d) // (of a half line the other half follows)
+            vraw[d] = load_codes<ONCE && LAYOUT != kHalf>(vp + d * 16 * block);
 
         float4_t sc[RT][4];
 #pragma unroll
@@ -305,7 +310,7 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
                 top = fmaxf(top, x[e]);
             top = max_xor32(max_xor16(top));
             if (__any(top > m[t] + kLazy)) {
-                const float next = fmaxf(m[t], top);
+                const float next = top > m[t] + kLazy ? top : m[t]; // (a row moves for its own sake only)
                 const float alpha = next == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - next);
                 m[t] = next;
                 l[t] *= alpha;
@@ -396,7 +401,7 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
 
 // One workgroup a unit: for contexts that one workgroup reads fast enough,
 // or units enough to fill the chip many times over.
-template <int D, int RT, int DT, int LAYOUT>
+template <int D, int RT, int DT, int LAYOUT, bool ONCE>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a, int units)
 {
     __shared__ __attribute__((aligned(16))) SplitLds<D, RT> lds;
@@ -404,7 +409,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a, i
     const int rb = (int)blockIdx.x / a.kv_heads;
     Piece p = {s, (int)blockIdx.y, (int)blockIdx.x - rb * a.kv_heads, rb * 16 * RT, s.lo, s.hi, nullptr};
     if (p.row0 < s.rows)
-        split_piece<D, RT, DT, LAYOUT>(a, p, lds);
+        split_piece<D, RT, DT, LAYOUT, ONCE>(a, p, lds);
 }
 
 // The tiles of all units in a row, cut into equal ranges, split_groups a CU:
@@ -418,7 +423,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a, i
 // (requests + 1 of them); from the next multiple of four words on, two pieces a range.
 __device__ __host__ __forceinline__ int64_t parts_offset(int64_t requests) { return (requests + 2 + 3) / 4 * 4; }
 
-template <int D, int RT, int DT, int LAYOUT>
+template <int D, int RT, int DT, int LAYOUT, bool ONCE>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a, int units)
 {
     constexpr int NW = kWaves, NT = 64 * NW;
@@ -507,7 +512,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
     range.s.cost = __builtin_amdgcn_readfirstlane(found.cost);
     Piece p;
     while (range.template next<D, RT>(a, units, p))
-        split_piece<D, RT, DT, LAYOUT>(a, p, lds);
+        split_piece<D, RT, DT, LAYOUT, ONCE>(a, p, lds);
 }
 
 // Joins the pieces of a row: one workgroup a row, its four waves over the
@@ -590,9 +595,24 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int uni
         *out = (uint16_t)Act<DT>::pack(acc[0] * n, 0.0f);
 }
 
-bool prompt_preferred(int64_t requests, int64_t kv_heads, int64_t group, int64_t max_new)
+// Whether the prompt kernel is the faster one (it takes 128 channels).  Its
+// workgroups of 256 rows take 2.3 us for 64 keys, one a CU; the split kernel
+// takes about 6 us for 32 rows in each of eight waves a CU, and shares any work
+// out evenly.  So up to 32 rows a key head, and where the row blocks leave too
+// many CUs idle, the split kernel runs.  Both, us, 32 query heads on 2 key
+// heads: one request of 512 tokens behind 8000 235 / 141, of 1024 alone 38 / 55,
+// 16 of up to 100 behind up to 3000 91 / 132, eight of up to 1024 71 / 108.
+// With 64 channels the split kernel was the faster everywhere from 40 tokens
+// to eight prompts of up to 4096 (an eight-wave prompt kernel: 264 / 268 there,
+// 47 / 34 for eight of up to 1024).
+bool prompt_preferred(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t max_new)
 {
-    return max_new * group > 32;
+    if (max_new * group <= 32 || head_dim != 128)
+        return false;
+    const double cus = device_cu_count();
+    const double rows = (double)tokens * (double)group;
+    const double blocks = (rows / 256 + (double)requests) * (double)kv_heads, units = (rows / 32 + (double)requests) * (double)kv_heads;
+    return 2.3 * (blocks < cus ? 1.0 : blocks / cus) <= 6.0 * units / (8 * cus);
 }
 
 struct SplitShape {
@@ -612,6 +632,10 @@ SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int
         span = window + max_new + kTile;
     const int64_t tiles = (span + kTile - 1) / kTile, all = (tiles + kUnitCost) * requests * p.units;
     p.groups = device_cu_count() * split_groups((int)head_dim, p.rt);
+    // One workgroup a unit where a unit is short, or where units fill the chip
+    // some times over (then the dispatch balances them, also the unequal row
+    // blocks of prompts, and nothing has to be joined: 1205 units of 65 tiles
+    // take 111 us so, and 191 and 30 for the join in ranges).
     if (tiles <= 8 || all >= (int64_t(1) << 31) - (1 << 20) || requests * p.units >= 4 * (int64_t)p.groups)
         p.groups = 0;
     else if (all < kMinRange * (int64_t)p.groups)
@@ -619,14 +643,14 @@ SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int
     return p;
 }
 
-template <int D, int RT, int DT, int LAYOUT>
+template <int D, int RT, int DT, int LAYOUT, bool ONCE>
 hipError_t launch_split(const KvAttnArgs &a, const SplitShape &p, hipStream_t stream)
 {
     if (p.groups == 0) {
-        kv_unit_kernel<D, RT, DT, LAYOUT><<<dim3((unsigned)p.units, (unsigned)a.requests), dim3(64 * kWaves), 0, stream>>>(a, p.units);
+        kv_unit_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.units, (unsigned)a.requests), dim3(64 * kWaves), 0, stream>>>(a, p.units);
         return hipGetLastError();
     }
-    kv_stream_kernel<D, RT, DT, LAYOUT><<<dim3((unsigned)p.groups), dim3(64 * kWaves), 0, stream>>>(a, p.units);
+    kv_stream_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.groups), dim3(64 * kWaves), 0, stream>>>(a, p.units);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
@@ -635,19 +659,22 @@ hipError_t launch_split(const KvAttnArgs &a, const SplitShape &p, hipStream_t st
     return hipGetLastError();
 }
 
-template <int D, int RT, int DT>
+template <int D, int RT, int DT, bool ONCE>
 hipError_t launch_layout(const KvAttnArgs &a, const SplitShape &p, hipStream_t stream)
 {
     if (a.block_shift < 6)
-        return launch_split<D, RT, DT, kNarrow>(a, p, stream);
-    return a.block_shift == 6 ? launch_split<D, RT, DT, kWhole>(a, p, stream) : launch_split<D, RT, DT, kHalf>(a, p, stream);
+        return launch_split<D, RT, DT, kNarrow, ONCE>(a, p, stream);
+    return a.block_shift == 6 ? launch_split<D, RT, DT, kWhole, ONCE>(a, p, stream)
+                              : launch_split<D, RT, DT, kHalf, ONCE>(a, p, stream);
 }
 
 template <int D, int DT>
 hipError_t launch_dim(const KvAttnArgs &a, hipStream_t stream)
 {
     const SplitShape p = split_shape(a.requests, a.kv_heads, D, a.group, a.max_new, a.max_context, a.window);
-    return p.rt == 1 ? launch_layout<D, 1, DT>(a, p, stream) : launch_layout<D, 2, DT>(a, p, stream);
+    if (p.rt == 1)
+        return launch_layout<D, 1, DT, true>(a, p, stream);
+    return p.units == a.kv_heads ? launch_layout<D, 2, DT, true>(a, p, stream) : launch_layout<D, 2, DT, false>(a, p, stream);
 }
 
 } // namespace
@@ -655,7 +682,7 @@ hipError_t launch_dim(const KvAttnArgs &a, hipStream_t stream)
 int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                int64_t requests, int64_t max_new, int64_t max_context, int64_t window)
 {
-    if (prompt_preferred(requests, kv_heads, q_heads / kv_heads, max_new))
+    if (prompt_preferred(tokens, requests, kv_heads, head_dim, q_heads / kv_heads, max_new))
         return 0;
     const SplitShape p = split_shape(requests, kv_heads, head_dim, q_heads / kv_heads, max_new, max_context, window);
     if (p.groups == 0)
@@ -665,7 +692,7 @@ int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, int dtype, hipStream_t stream)
 {
-    if (prompt_preferred(a.requests, a.kv_heads, a.group, a.max_new))
+    if (prompt_preferred(a.tokens, a.requests, a.kv_heads, a.head_dim, a.group, a.max_new))
         return launch_kv_prompt(a, dtype, stream);
     if (a.head_dim == 64)
         return dtype == QW_F16 ? launch_dim<64, QW_F16>(a, stream) : launch_dim<64, QW_BF16>(a, stream);

@@ -88,7 +88,7 @@ int device_cu_count(); // qw_api.hip
 int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                int64_t requests, int64_t max_new, int64_t max_context, int64_t window);
 hipError_t launch_kv_attention(const KvAttnArgs &a, int dtype, hipStream_t stream);
-// The kernel for many query rows (kv_prompt.hip), any sizes.
+// The kernel for many query rows (kv_prompt.hip): 128 channels, else any sizes.
 hipError_t launch_kv_prompt(const KvAttnArgs &a, int dtype, hipStream_t stream);
 
 } // namespace qw

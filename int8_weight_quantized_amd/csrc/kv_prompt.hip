@@ -29,41 +29,83 @@ namespace qw {
 
 namespace {
 
+constexpr int D = 128;
+constexpr int STEPS = D / 16; // of the first product
+constexpr int DTILES = D / 32;
 constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves; // query rows of a workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 64;
-constexpr float kLazy = 8.0f;
+constexpr int kSlots = 65; // of a fragment: a lane each, and one so that fragments begin at different banks
+constexpr float kLarge = 32768.0f; // of weights' sums: below it none overflows fp16
+constexpr int kAhead = 4; // fragments read ahead of the matrix instructions
+constexpr int kSegment = 64; // tiles whose scales are fetched at once
+constexpr int kFirst = 3; // number of the first tile: its buffers have index 0 (modulo 3)
 constexpr float kNothing = -3e38f; // the threshold of a row that has seen no key
 
-template <int D>
 union PromptLds {
     struct {
-        half8_t k[2][kTile * D / 8]; // [32-key half][16-channel step][slot]
-        half8_t v[2][kTile * D / 8]; // [32-channel tile][16-key step][slot]
-        float4_t scale[2][4];        // per 16 keys: key scale * log2(e) * softmax scale, log2 of the value scale, its inverse
+        half8_t k[3][D / 8][kSlots]; // [32-key half][16-channel step][lane]
+        half8_t v[3][D / 8][kSlots]; // [32-channel tile][16-key step][lane]
+        // per 16 keys: key scale * log2(e) * softmax scale, log2 of the value
+        // scale, its inverse; of two segments of the keys
+        float4_t scale[2][kSegment * 4];
     };
     uint16_t out[kRows][D + 8];
+    struct {
+        int sums[kWaves], found[2];
+    };
 };
 
-template <int D, int DT>
-__global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a, int row_blocks)
+template <int DT>
+__global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
 {
-    constexpr int STEPS = D / 16; // of the first product
-    constexpr int DTILES = D / 32;
-    __shared__ __attribute__((aligned(16))) PromptLds<D> lds;
+    __shared__ __attribute__((aligned(16))) PromptLds lds;
 
     const int tid = threadIdx.x, lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
-    // row blocks from the last to the first: under a causal mask the longest first
-    const int per_block = a.requests * a.kv_heads;
-    const int rb = row_blocks - 1 - (int)blockIdx.x / per_block;
-    const int unit = (int)blockIdx.x % per_block;
-    const int r = unit / a.kv_heads, kvh = unit - r * a.kv_heads;
+    // Which request and row block.  Workgroups that have nothing to do would
+    // hold up the dispatch (each waits for a CU's LDS, and workgroups go round
+    // the shader engines whatever they hold: with one long request among four,
+    // 64 of 256 CUs worked), so the row blocks of all requests lie in a row, and
+    // the host bounds their number by the tokens'.  Within a request the last
+    // rows come first: under a causal mask they have the most keys.
+    int target = (int)blockIdx.x / a.kv_heads;
+    const int kvh = (int)blockIdx.x - target * a.kv_heads;
+    for (int base = 0;; base += kThreads) {
+        if (base >= a.requests)
+            return; // (the bound's slack)
+        const int mine = base + tid;
+        const KvRequest q = kv_request(a, mine < a.requests ? mine : a.requests - 1);
+        const int blocks = mine < a.requests ? (q.rows + kRows - 1) / kRows : 0;
+        int upto = blocks;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(upto, d);
+            upto += lane >= d ? up : 0;
+        }
+        if (lane == 63)
+            lds.sums[wave] = upto;
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            upto += w < wave ? lds.sums[w] : 0;
+            total += lds.sums[w];
+        }
+        if (target < upto && target >= upto - blocks) {
+            lds.found[0] = mine;
+            lds.found[1] = upto - 1 - target;
+        }
+        __syncthreads();
+        if (target < total)
+            break;
+        target -= total;
+    }
+    const int r = __builtin_amdgcn_readfirstlane(lds.found[0]);
+    const int row0 = __builtin_amdgcn_readfirstlane(lds.found[1]) * kRows;
     const KvRequest s = kv_request(a, r);
-    const int row0 = rb * kRows;
-    if (row0 >= s.rows)
-        return;
+    __syncthreads(); // lds is the tiles' from here on
     const int last_row = row0 + kRows < s.rows ? row0 + kRows - 1 : s.rows - 1;
     const int first_i = row0 / a.group, last_i = last_row / a.group;
     // keys that some row of the block sees, and keys that every one does
@@ -73,66 +115,72 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a, in
     const int all_lo = a.window ? s.past + last_i - a.window + 1 : 0;
 
     // ---- staging: what this thread brings into LDS -------------------------
-    const int block = 1 << a.block_shift;
+    // A piece of 16 bytes of each: 16 channels of a key (kt, kc) and 16 keys of
+    // a channel (vd, vk).  They are dealt out so that a wave's pieces of a tile
+    // lie in one block, whatever the block size: its address is scalar work, and
+    // a lane's offset in the block never changes.  Keys are fetched a tile ahead
+    // of the values.  The staging has no branches: the compiler could not count
+    // the loads in flight across them, and would wait for all (1000 cycles a
+    // tile).
+    const int shift = a.block_shift, block = 1 << shift;
     const int64_t head_bytes = (int64_t)block * D;
     const int32_t *table = a.block_table + (int64_t)r * a.table_width;
-    constexpr int KP = kTile * D / 16; // 16-byte pieces of an operand's tile
-    constexpr bool kBoth = KP == kThreads; // a piece of each a thread; otherwise half the threads bring keys, half values
-    const bool brings_k = kBoth || tid < KP, brings_v = kBoth || tid >= KP;
-    const int kp = kBoth ? tid : (tid & (KP - 1)); // which piece
-    const int kt = kp / (D / 16), kc = kp % (D / 16); // key of the tile, 16-channel step
-    const int vd = kp >> 2, vk = kp & 3;            // channel, 16-key step
-    const int kgroup = kt >> 4;
-    // slots: row m of the first product's tile holds key u of 32
-    const int u = kt & 31;
-    const int m = (u & 3) + 16 * (u >> 4) + 8 * ((u >> 2) & 1) + 4 * ((u >> 3) & 1);
-    const int kslot = ((kt >> 5) * STEPS + kc) * 64, vslot = ((vd >> 5) * 4 + vk) * 64;
-    const int k0 = kslot + (m ^ (kc & 7)), k1 = kslot + ((m + 32) ^ (kc & 7));
-    const int v0 = vslot + ((vd & 31) ^ (vk << 1)), v1 = vslot + (((vd & 31) + 32) ^ (vk << 1));
-
-    auto look = [&](int j) { return j < end ? table[j >> a.block_shift] : -1; };
+    static_assert(kTile * D / 16 == kThreads, "a piece of each operand a thread");
+    const int side = shift < 6 ? shift - 4 : 2; // log2 of a block's pieces of one channel, of a tile
+    const int kt = tid / (D / 16), kc = tid % (D / 16);
+    const int vb = tid >> side >> 7, vd = (tid >> side) & (D - 1), vk = (tid & ((1 << side) - 1)) + (vb << side);
+    const uint32_t k_at = (uint32_t)((kt & (block - 1)) * D + kc * 16), v_at = (uint32_t)(vd * block + ((vk * 16) & (block - 1)));
+    const int k_first = __builtin_amdgcn_readfirstlane(kt & ~15), v_first = __builtin_amdgcn_readfirstlane((vb << side) * 16);
+    // row m of the first product's tile holds key u of 32
+    const int u = kt & 31, m = (u & 3) + 16 * (u >> 4) + 8 * ((u >> 2) & 1) + 4 * ((u >> 3) & 1);
     auto known = [&](int32_t id) { return id >= 0 && id < a.num_blocks; };
     auto row_of = [&](int32_t id) { return (int64_t)(known(id) ? id : 0) * a.kv_heads + kvh; };
-    u32x4_t kraw = {0, 0, 0, 0}, vraw = {0, 0, 0, 0};
-    float ks = 0.0f, vs = 0.0f;
-    bool ok = false;
-    int32_t kid = -1, vid = -1, sid = -1; // blocks of this thread's pieces and of 16-key group tid % 4
-    auto look_all = [&](int base) {
-        kid = brings_k ? look(base + kgroup * 16) : -1;
-        vid = brings_v ? look(base + vk * 16) : -1;
-        sid = look(base + (tid & 3) * 16);
+    // The block of key j (of the last key, behind it: read and masked).
+    auto look = [&](int j) { return table[(j < end ? j : end - 1) >> shift]; };
+    u32x4_t kraw, vraw;
+    int32_t kid, vid; // blocks of the next pieces
+    auto look_k = [&](int base) { kid = look(base + k_first); };
+    auto look_v = [&](int base) { vid = look(base + v_first); };
+    auto fetch_k = [&](int base) {
+        kraw = *reinterpret_cast<const u32x4_t *>(a.k_cache + row_of(__builtin_amdgcn_readfirstlane(kid)) * head_bytes +
+                                                  (base & (block - 1)) * D + k_at);
     };
-    auto load = [&](int base) {
-        if (brings_k)
-            kraw = *reinterpret_cast<const u32x4_t *>(a.k_cache + row_of(kid) * head_bytes +
-                                                      (uint32_t)(((base + kt) & (block - 1)) * D + kc * 16));
-        if (brings_v)
-            vraw = *reinterpret_cast<const u32x4_t *>(a.v_cache + row_of(vid) * head_bytes +
-                                                      (uint32_t)(vd * block + ((base + vk * 16) & (block - 1))));
-        ks = a.k_scales[row_of(sid)];
-        vs = a.v_scales[row_of(sid)];
-        ok = known(sid);
+    auto fetch_v = [&](int base) {
+        vraw = *reinterpret_cast<const u32x4_t *>(a.v_cache + row_of(__builtin_amdgcn_readfirstlane(vid)) * head_bytes +
+                                                  (base & (block - 1)) + v_at);
     };
-    auto store = [&](int buf) {
-        if (brings_k) {
-            lds.k[buf][k0] = i8x8_to_half8(kraw.x, kraw.y);
-            lds.k[buf][k1] = i8x8_to_half8(kraw.z, kraw.w);
-        }
-        if (brings_v) {
-            lds.v[buf][v0] = i8x8_to_half8(vraw.x, vraw.y);
-            lds.v[buf][v1] = i8x8_to_half8(vraw.z, vraw.w);
-        }
-        if (tid < 4) {
-            const float sc = fmaxf(vs, kKvScaleFloor);
+    auto put_k = [&](int tile) {
+        half8_t *at = &lds.k[tile % 3][(kt >> 5) * STEPS + kc][m];
+        at[0] = i8x8_to_half8(kraw.x, kraw.y);
+        at[32] = i8x8_to_half8(kraw.z, kraw.w);
+    };
+    auto put_v = [&](int tile) {
+        half8_t *at = &lds.v[tile % 3][(vd >> 5) * 4 + vk][vd & 31];
+        at[0] = i8x8_to_half8(vraw.x, vraw.y);
+        at[32] = i8x8_to_half8(vraw.z, vraw.w);
+    };
+    // The scales of a segment, one 16-key group a thread: log2 and inverse once,
+    // not by every wave for every tile.
+    auto segment_scales = [&](int segment) {
+        const int key = begin + segment * (kSegment * kTile) + tid * 16;
+        if (tid < kSegment * 4 && key < end) {
+            const int32_t at = table[key >> shift];
+            const float ks = a.k_scales[row_of(at)], vs = fmaxf(a.v_scales[row_of(at)], kKvScaleFloor);
             // (a group without a block: scores of -inf, whatever its codes)
-            lds.scale[buf][tid] = ok ? (float4_t){ks * a.scale_log2, __log2f(sc), 1.0f / sc, 0.0f}
-                                     : (float4_t){0.0f, -INFINITY, 0.0f, 0.0f};
+            lds.scale[segment & 1][tid] = known(at) ? (float4_t){ks * a.scale_log2, __builtin_amdgcn_logf(vs), 1.0f / vs, 0.0f}
+                                                    : (float4_t){0.0f, -INFINITY, 0.0f, 0.0f};
         }
     };
-
-    look_all(begin);
-    if (begin < end)
-        load(begin);
+    // Puts down the values of tile number `tile` (at key `base`) and the keys of
+    // the next, and asks for what the next call puts down.
+    auto stage = [&](int tile, int base) {
+        put_k(tile + 1);
+        put_v(tile);
+        fetch_k(base + 2 * kTile);
+        fetch_v(base + kTile);
+        look_k(base + 3 * kTile);
+        look_v(base + 2 * kTile);
+    };
 
     // ---- this wave's query rows --------------------------------------------
     const int row = row0 + wave * 32 + col;
@@ -171,100 +219,166 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a, in
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             o[d][i] = 0.0f;
-    // A row's reference moves when a score exceeds it by the threshold: kLazy,
-    // or anything while the row has seen no key.
-    float ref = 0.0f, above = kNothing, l = 0.0f;
+    float ref = 0.0f, l = 0.0f;
+    bool seen = !in; // a key; both lanes of a row agree
 
-    look_all(begin + kTile);
-    if (begin < end)
-        store(0);
-    __syncthreads();
-
-    int buf = 0;
-    for (int base = begin; base < end; base += kTile, buf ^= 1) {
-        const bool more = base + kTile < end;
-        if (more) {
-            load(base + kTile);
-            look_all(base + 2 * kTile);
-        }
-
-        float16_t sc[2];
+    float16_t sc[2];
+    half8_t p[4];
+    // Matrix phase: the second product of a tile, and the first product of the
+    // next.  Fragments are read kAhead before their use.  (The empty asm keeps a
+    // buffer's address in one register, so that fragments are constant offsets
+    // from it; folded into them it would leave the instruction's range.)
+    typedef __attribute__((address_space(3))) const half8_t lds_half8;
+    auto key_product = [&](int buf) {
+        lds_half8 *k = (lds_half8 *)&lds.k[buf][0][lane];
+        asm("" : "+v"(k));
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 sc[t][i] = 0.0f;
 #pragma unroll
-            for (int c = 0; c < STEPS; ++c)
-                sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lds.k[buf][(t * STEPS + c) * 64 + (lane ^ (c & 7))], q[c], sc[t],
-                                                               0, 0, 0);
-        }
-
-        // exponents relative to the reference; 8 scores a lane share a scale
-        float4_t g[4];
+        for (int c = 0; c < STEPS; ++c)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[(t * STEPS + c) * kSlots], q[c], sc[t], 0, 0, 0);
+    };
+    auto value_product = [&](int buf) {
+        lds_half8 *v = (lds_half8 *)&lds.v[buf][0][lane];
+        asm("" : "+v"(v));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            g[j] = lds.scale[buf][j];
-        const bool whole = base >= all_lo && base + kTile <= all_hi;
-        float x[32];
-        auto exponents = [&]() {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float c = g[j].x * down, b = g[j].y - ref;
+            for (int d = 0; d < DTILES; ++d)
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[(d * 4 + j) * kSlots], p[j], o[d], 0, 0, 0);
+    };
+    auto order = [&]() {
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0); // LDS reads
+#pragma unroll
+        for (int i = 0; i < 4 * DTILES + 2 * STEPS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // a matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+    };
+    // Softmax phase: the weights of a tile.  A row's reference moves when its
+    // weights get large (their sum tells, without a maximum over them), and at
+    // the first tile of which the row sees a key.
+    float4_t g[4]; // the tile's scales, read while the matrix instructions run
+    auto read_scales = [&](int tile) {
+        const int n = tile - kFirst;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            g[j] = lds.scale[n / kSegment & 1][(n & (kSegment - 1)) * 4 + j];
+    };
+    auto softmax = [&](int base) {
+        float inv[4], sum[4], y[32];
+        // scores become exponents relative to the reference (8 scores of a lane
+        // share a scale)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float c = g[j].x * down, b = g[j].y - ref;
+            inv[j] = g[j].z;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sc[j >> 1][(j & 1) * 8 + e] = fmaf(sc[j >> 1][(j & 1) * 8 + e], c, b);
+        }
+        if (base < all_lo || base + kTile > all_hi) {
+            const int lo = lim_lo - base - h * 8, hi = lim_hi - base - h * 8;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    x[8 * j + e] = fmaf(sc[j >> 1][(j & 1) * 8 + e], c, b);
-            }
-            if (!whole) {
+                    if (j * 16 + e < lo || j * 16 + e >= hi)
+                        sc[j >> 1][(j & 1) * 8 + e] = -INFINITY;
+        }
+        auto weights = [&]() {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                sum[j] = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int at = base + j * 16 + h * 8 + e;
-                        x[8 * j + e] = at >= lim_lo && at < lim_hi ? x[8 * j + e] : -INFINITY;
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    y[8 * j + e] = __builtin_amdgcn_exp2f(sc[j >> 1][(j & 1) * 8 + e]);
+                    sum[j] += y[8 * j + e];
+                }
             }
         };
-        exponents();
-        float top = x[0];
+        weights();
+        float most = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
+        if (__any(!seen || most >= kLarge)) {
+            // (a row moves for its own sake only: no result depends on which rows
+            // share a wave)
+            most = max_xor32(most);
+            float top = -INFINITY;
 #pragma unroll
-        for (int e = 1; e < 32; ++e)
-            top = fmaxf(top, x[e]);
-        if (__any(top > above)) {
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    top = fmaxf(top, sc[t][i]);
             top = max_xor32(top);
-            const bool first = above == kNothing, seen = top > kNothing;
-            const float up = first ? (seen ? top : 0.0f) : fmaxf(top, 0.0f); // the new reference lies so far above the old
-            const float alpha = first ? 1.0f : __builtin_amdgcn_exp2f(-up);
+            const float up = seen ? (most >= kLarge ? top : 0.0f) : (top > kNothing ? top : 0.0f); // the new reference lies so far above the old
+            const float alpha = seen ? __builtin_amdgcn_exp2f(-up) : 1.0f;
             ref += up;
-            above = seen || !first ? kLazy : kNothing;
+            seen = seen || top > kNothing;
             l *= alpha;
 #pragma unroll
             for (int d = 0; d < DTILES; ++d)
                 o[d] *= alpha;
-            exponents();
+            sc[0] -= up;
+            sc[1] -= up;
+            weights();
         }
-        half8_t p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float sum = 0.0f;
+            l = fmaf(sum[j], inv[j], l);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = __builtin_amdgcn_exp2f(x[8 * j + e]);
-                sum += y;
-                p[j][e] = (_Float16)y; // to nearest: 2^-11 of a weight at most
-            }
-            l = fmaf(sum, g[j].z, l);
+            for (int e = 0; e < 8; ++e)
+                p[j][e] = (_Float16)y[8 * j + e]; // to nearest: 2^-11 of a weight at most
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int d = 0; d < DTILES; ++d)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lds.v[buf][(d * 4 + j) * 64 + (lane ^ (j << 1))], p[j], o[d], 0,
-                                                              0, 0);
-        if (more)
-            store(buf ^ 1);
+    };
+
+    // The first two tiles' keys, the first one's values; what follows is asked
+    // for.
+    if (begin < end) {
+        look_k(begin);
+        look_v(begin);
+        fetch_k(begin);
+        look_k(begin + kTile);
+        put_k(kFirst);
+        fetch_k(begin + kTile);
+        fetch_v(begin);
+        look_k(begin + 2 * kTile);
+        look_v(begin + kTile);
+        segment_scales(0);
+        stage(kFirst, begin);
+    }
+    __syncthreads();
+
+    // The two waves of a SIMD take turns: while waves 0 to 3 are in a matrix
+    // phase, waves 4 to 7 are in the softmax phase of the tile before, and the
+    // other way round.
+    const bool second = wave >= 4;
+    if (second)
+        __syncthreads();
+    key_product(kFirst % 3);
+    read_scales(kFirst);
+    __syncthreads();
+    int tile = kFirst;
+    for (int base = begin; base < end; base += kTile, ++tile) {
+        softmax(base);
+        stage(tile + 1, base + kTile);
+        if (((tile - kFirst) & (kSegment - 1)) == kSegment / 2)
+            segment_scales((tile - kFirst) / kSegment + 1);
+        __syncthreads();
+        __builtin_amdgcn_s_setprio(1);
+        value_product(tile % 3);
+        key_product((tile + 1) % 3); // (behind the last tile: not used)
+        order();
+        read_scales(tile + 1);
+        __builtin_amdgcn_s_setprio(0);
         __syncthreads();
     }
+    if (!second)
+        __syncthreads();
 
     // ---- rows to the output, through LDS for whole lines -------------------
     l = add_xor32(l);
@@ -293,19 +407,14 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a, in
 
 hipError_t launch_kv_prompt(const KvAttnArgs &a, int dtype, hipStream_t stream)
 {
-    const int row_blocks = (int)(((int64_t)a.max_new * a.group + kRows - 1) / kRows);
-    const dim3 grid((unsigned)((int64_t)row_blocks * a.requests * a.kv_heads));
-    if (a.head_dim == 64) {
-        if (dtype == QW_F16)
-            kv_prompt_kernel<64, QW_F16><<<grid, dim3(kThreads), 0, stream>>>(a, row_blocks);
-        else
-            kv_prompt_kernel<64, QW_BF16><<<grid, dim3(kThreads), 0, stream>>>(a, row_blocks);
-    } else {
-        if (dtype == QW_F16)
-            kv_prompt_kernel<128, QW_F16><<<grid, dim3(kThreads), 0, stream>>>(a, row_blocks);
-        else
-            kv_prompt_kernel<128, QW_BF16><<<grid, dim3(kThreads), 0, stream>>>(a, row_blocks);
-    }
+    // row blocks of all requests: full ones of the tokens' rows, and a last one each
+    const int64_t each = ((int64_t)a.max_new * a.group + kRows - 1) / kRows * a.requests;
+    const int64_t full = (int64_t)a.tokens * a.group / kRows + a.requests;
+    const dim3 grid((unsigned)((each < full ? each : full) * a.kv_heads));
+    if (dtype == QW_F16)
+        kv_prompt_kernel<QW_F16><<<grid, dim3(kThreads), 0, stream>>>(a);
+    else
+        kv_prompt_kernel<QW_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 
