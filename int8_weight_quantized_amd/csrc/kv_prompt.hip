@@ -160,11 +160,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
         at[32] = i8x8_to_half8(vraw.z, vraw.w);
     };
     // The scales of a segment, one 16-key group a thread: log2 and inverse once,
-    // not by every wave for every tile.
+    // not by every wave for every tile.  Groups behind the last key get its
+    // block's: their weights are 0, and 0 has to be multiplied by a finite inverse.
     auto segment_scales = [&](int segment) {
-        const int key = begin + segment * (kSegment * kTile) + tid * 16;
-        if (tid < kSegment * 4 && key < end) {
-            const int32_t at = table[key >> shift];
+        if (tid < kSegment * 4) {
+            const int32_t at = look(begin + segment * (kSegment * kTile) + tid * 16);
             const float ks = a.k_scales[row_of(at)], vs = fmaxf(a.v_scales[row_of(at)], kKvScaleFloor);
             // (a group without a block: scores of -inf, whatever its codes)
             lds.scale[segment & 1][tid] = known(at) ? (float4_t){ks * a.scale_log2, __builtin_amdgcn_logf(vs), 1.0f / vs, 0.0f}

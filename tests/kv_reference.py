@@ -176,6 +176,50 @@ def attention(q, cache, table, context, cu, max_new, scale, causal=True, window=
     return out, mass, reach, tail
 
 
+def attention_rows(q, cache, table, context, cu, max_new, scale, causal=True, window=0):
+    """attention() with the rows of a key head taken at once, for many rows."""
+    k_cache, v_cache, ks, vs = cache
+    blocks, kv, block, dim = k_cache.shape
+    T, heads, _ = q.shape
+    group = heads // kv
+    q = q.astype(np.float64)
+    out = np.full(q.shape, np.nan)
+    mass = np.zeros(q.shape)
+    reach = np.zeros((T, heads, 1))
+    tail = np.zeros((T, heads, 1))
+    for r in range(table.shape[0]):
+        t0, total = int(cu[r]), int(cu[r + 1]) - int(cu[r])
+        n = min(total, max_new)
+        ctx = min(int(context[r]), table.shape[1] * block)
+        if n <= 0:
+            continue
+        if ctx <= 0:
+            out[t0:t0 + n] = 0.0
+            continue
+        ids = table[r, :-(-ctx // block)].astype(np.int64)
+        ok = (ids >= 0) & (ids < blocks)
+        ids = np.where(ok, ids, 0)
+        there = np.repeat(ok, block)[:ctx]
+        j, p = np.arange(ctx), (ctx - total + np.arange(n))[:, None]
+        see = there & (j <= p if causal else True) & (j > p - window if window else True)
+        see = np.repeat(np.broadcast_to(see, (n, ctx)), group, 0)
+        some = see.any(1)
+        for h in range(kv):
+            K = (k_cache[ids, h].astype(np.float64) * ks[ids, h].astype(np.float64)[:, None, None]).reshape(-1, dim)[:ctx]
+            V = (v_cache[ids, h].astype(np.float64) * vs[ids, h].astype(np.float64)[:, None, None]).swapaxes(1, 2).reshape(-1, dim)[:ctx]
+            K, V = np.where(there[:, None], K, 0.0), np.where(there[:, None], V, 0.0)
+            x = q[t0:t0 + n, h * group:(h + 1) * group].reshape(-1, dim)
+            s = np.where(see, scale * (x @ K.T), -np.inf)
+            w = np.exp(s - np.where(some, s.max(1), 0.0)[:, None])
+            w /= np.where(some, w.sum(1), 1.0)[:, None]
+            at = (slice(t0, t0 + n), slice(h * group, (h + 1) * group))
+            out[at] = (w @ V).reshape(n, group, dim)
+            mass[at] = (w @ np.abs(V)).reshape(n, group, dim)
+            reach[at] = (abs(scale) * np.where(see, np.abs(x) @ np.abs(K).T, 0.0).max(1)).reshape(n, group, 1)
+            tail[at] = (see.sum(1) * np.where(see, np.abs(V).max(1), 0.0).max(1)).reshape(n, group, 1)
+    return out, mass, reach, tail
+
+
 def attention_tolerance(out, mass, reach, tail, dim, unit):
     """One rounding of the output (`unit` of it); one fp16 rounding of each weight (2^-11 of
     it, 2^-25 where it is subnormal, relative to a largest weight of at least
