@@ -13,12 +13,14 @@
 // token at offset 0 starts the block afresh, and nothing before the run is
 // read unless the scale grows.
 //
-// Bound by HBM for prompts (2 bytes in, 1 byte out an element) and by
-// latency for single tokens.  A wave owns a run (all four waves of the
-// workgroup, where the workgroup's window of tokens holds only one): it
-// reads the run twice, for the maximum and for the codes; the second read
-// comes from L2.  Values are stored transposed: a lane packs 16 tokens of
-// two channels into two 16-byte stores.
+// Bound by HBM for prompts (2 bytes in, 1 byte out an element: 4 prompts of
+// 4000 tokens, 8 heads of 128, in 26 us, 3.8 TB/s) and by latency for single
+// tokens (64 of them: 4.5 us, of which a launch is about 4).  A run is read
+// once, into the registers of a wave or of a workgroup, which hold it from
+// the maximum to the codes (read twice, from L2 the second time, with windows
+// of 16 tokens and general divisions: 62 us for those prompts).  Values are
+// stored transposed: a lane packs 16 tokens of two channels into two 16-byte
+// stores.
 //
 // This unit is compiled without floating-point contraction: codes and
 // scales are bit-exact by the formulas above.
@@ -31,9 +33,24 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t code_of(float x, float s)
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// x / s correctly rounded, from the correctly rounded inverse of s: the
+// residual of x * inverse is exact, and one step along it lands on the
+// nearest float (checked for every significand of s with every 11-bit one of
+// x and quotients of 2^-2 to 2^8; below, the code is 0 whatever the last bit).
+// A third of a general division's instructions.
+struct Scale {
+    float s, inverse; // both 0 for a run of zeros
+};
+
+__device__ __forceinline__ uint32_t code_of(float x, Scale k)
 {
-    const float r = fminf(fmaxf(rintf(x / s), -127.0f), 127.0f);
+    const float y = x * k.inverse;
+    const float r = fminf(fmaxf(rintf(fmaf(fmaf(-y, k.s, x), k.inverse, y)), -127.0f), 127.0f);
     return (uint32_t)(int)r & 0xffu;
 }
 
@@ -48,14 +65,18 @@ __device__ __forceinline__ uint32_t rescaled4(uint32_t w, float ratio)
            rescaled(w >> 24, ratio) << 24;
 }
 
+// The low n bytes.
+__device__ __forceinline__ uint32_t low_bytes(int n) { return n >= 4 ? ~0u : n > 0 ? (1u << (8 * n)) - 1 : 0u; }
+
 // One run of `len` tokens from token t on, at offset `off` of block `blk`,
 // for one head and for keys (VALUES false) or values, by NW waves (this one
-// is `wave` of them).
-template <int DT, int D, int NW, bool VALUES>
-__device__ void write_run(const KvCacheArgs &a, int64_t t, int64_t blk, int off, int len, int head, int wave, float *lds)
+// is `wave` of them).  MOST bounds the run: the block size, or 16 for a run
+// within one segment of 16 places.  Its elements stay in registers from the
+// maximum to the codes; loads beyond the run repeat its last token, so that
+// they need no branch.
+template <int DT, int D, int NW, int MOST, bool VALUES>
+__device__ __forceinline__ void write_run(const KvCacheArgs &a, int64_t t, int64_t blk, int off, int len, int head, int wave, float *lds)
 {
-    constexpr int LPT = D / 8;   // lanes a token of a 16-byte-a-lane read
-    constexpr int TPW = 64 / LPT; // tokens a wave reads at once
     const int lane = __lane_id();
     const int64_t block = int64_t(1) << a.block_shift;
     const int64_t stride = VALUES ? a.v_stride : a.k_stride;
@@ -64,16 +85,40 @@ __device__ void write_run(const KvCacheArgs &a, int64_t t, int64_t blk, int off,
     int8_t *codes = (VALUES ? a.v_cache : a.k_cache) + bh * block * D;
     float *scale = (VALUES ? a.v_scales : a.k_scales) + bh;
 
-    float top = 0.0f;
-    for (int i = wave * TPW + lane / LPT; i < len; i += NW * TPW) {
-        float f[8];
-        unpack8<DT>(*reinterpret_cast<const u32x4_t *>(x + i * stride + (lane & (LPT - 1)) * 8), f);
+    // keys: 16 bytes of a token a lane; values: two channels of 16 tokens a lane
+    constexpr int LPT = D / 8, TPW = 64 / LPT; // lanes a token, tokens a wave
+    constexpr int LPS = D / 2, SPW = 64 / LPS; // lanes a segment of 16 tokens, segments a wave
+    constexpr int N = VALUES ? (MOST / 16 + NW * SPW - 1) / (NW * SPW) : MOST / (NW * TPW);
+    constexpr int DWORDS = VALUES ? 16 : 4;
+    const int unit = VALUES ? wave * SPW + lane / LPS : wave * TPW + lane / LPT;
+    const int d = VALUES ? 2 * (lane & (LPS - 1)) : 8 * (lane & (LPT - 1));
+    const int first = MOST == 16 ? off & ~15 : 0; // place of the first segment
+    uint32_t raw[N][DWORDS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            top = fmaxf(top, fabsf(f[e]));
+    for (int n = 0; n < N; ++n) {
+        if (VALUES) {
+            const int lo = first + (n * NW * SPW + unit) * 16 - off;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int i = lo + j < 0 ? 0 : lo + j < len ? lo + j : len - 1;
+                raw[n][j] = *reinterpret_cast<const uint32_t *>(x + i * stride + d);
+            }
+        } else {
+            const int at = n * NW * TPW + unit, i = at < len ? at : len - 1;
+            const u32x4_t piece = *reinterpret_cast<const u32x4_t *>(x + i * stride + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                raw[n][j] = piece[j];
+        }
     }
-    top = wave_max_f32(top);
     const float was = off > 0 ? *scale : 0.0f;
+    float top = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < DWORDS; ++j)
+            top = fmaxf(top, fmaxf(fabsf(Act<DT>::lo(raw[n][j])), fabsf(Act<DT>::hi(raw[n][j]))));
+    top = wave_max_f32(top);
     if (NW > 1) {
         if (lane == 0)
             lds[wave] = top;
@@ -88,6 +133,7 @@ __device__ void write_run(const KvCacheArgs &a, int64_t t, int64_t blk, int off,
     s = grow ? s : was;
     const bool move = off > 0 && grow && was > 0.0f;
     const float ratio = move ? was / s : 1.0f;
+    const Scale k = {s, s > 0.0f ? 1.0f / s : 0.0f};
     if (wave == 0 && lane == 0)
         *scale = s;
 
@@ -99,72 +145,75 @@ __device__ void write_run(const KvCacheArgs &a, int64_t t, int64_t blk, int off,
                 *p = (u32x4_t){rescaled4(c.x, ratio), rescaled4(c.y, ratio), rescaled4(c.z, ratio),
                                rescaled4(c.w, ratio)};
             }
-        for (int i = wave * TPW + lane / LPT; i < len; i += NW * TPW) {
-            const int d = (lane & (LPT - 1)) * 8;
-            float f[8];
-            unpack8<DT>(*reinterpret_cast<const u32x4_t *>(x + i * stride + d), f);
-            u32x2_t c = {0, 0};
-            if (s > 0.0f) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    c.x |= code_of(f[e], s) << (8 * e);
-                    c.y |= code_of(f[4 + e], s) << (8 * e);
-                }
+        for (int n = 0; n < N; ++n) {
+            const int i = n * NW * TPW + unit;
+            if (i < len) {
+                u32x2_t c = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    c[e >> 1] |= (code_of(Act<DT>::lo(raw[n][e]), k) | code_of(Act<DT>::hi(raw[n][e]), k) << 8) << (16 * (e & 1));
+                *reinterpret_cast<u32x2_t *>(codes + (int64_t)(off + i) * D + d) = c;
             }
-            *reinterpret_cast<u32x2_t *>(codes + (int64_t)(off + i) * D + d) = c;
         }
     } else {
-        constexpr int LPS = D / 2;                        // lanes of a 16-token segment: two channels each
-        constexpr int SPW = LPS >= 64 ? 1 : 64 / LPS;     // segments a wave writes at once
-        constexpr int REP = LPS > 64 ? LPS / 64 : 1;      // channel groups of a wave
-        const int d_lane = 2 * (lane & (LPS < 64 ? LPS - 1 : 63));
-        const int first = move ? 0 : off / 16, last = (off + len - 1) / 16;
-        for (int seg = first + wave * SPW + lane / (LPS < 64 ? LPS : 64); seg <= last; seg += NW * SPW) {
-            const int lo = seg * 16;
+        if (MOST == 16 && move)
+            for (int lo = unit * 16; lo < first; lo += NW * SPW * 16)
 #pragma unroll
-            for (int rep = 0; rep < REP; ++rep) {
-                const int d = d_lane + rep * 128;
-                int8_t *row0 = codes + (int64_t)d * block + lo, *row1 = row0 + block;
-                u32x4_t c0 = {0, 0, 0, 0}, c1 = {0, 0, 0, 0};
-                // codes before the run stay (at the new scale); places behind it
-                // are not live, and keep what they hold
-                if (lo < off || lo + 16 > off + len) {
-                    c0 = *reinterpret_cast<const u32x4_t *>(row0);
-                    c1 = *reinterpret_cast<const u32x4_t *>(row1);
-                    if (move && lo < off) {
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const int n = off - lo - 4 * v; // codes of this word that lie before the run
-                            const uint32_t live = n >= 4 ? ~0u : (n > 0 ? (1u << (8 * n)) - 1 : 0u);
-                            c0[v] = (c0[v] & ~live) | (rescaled4(c0[v], ratio) & live);
-                            c1[v] = (c1[v] & ~live) | (rescaled4(c1[v], ratio) & live);
-                        }
-                    }
+                for (int v = 0; v < 2; ++v) {
+                    u32x4_t *p = reinterpret_cast<u32x4_t *>(codes + (int64_t)(d + v) * block + lo);
+                    const u32x4_t c = *p;
+                    *p = (u32x4_t){rescaled4(c.x, ratio), rescaled4(c.y, ratio), rescaled4(c.z, ratio),
+                                   rescaled4(c.w, ratio)};
                 }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int i = lo + j - off;
-                    if (i >= 0 && i < len) {
-                        const uint32_t pair = *reinterpret_cast<const uint32_t *>(x + i * stride + d);
-                        const uint32_t keep = ~(0xffu << (8 * (j & 3)));
-                        const uint32_t u = s > 0.0f ? code_of(Act<DT>::lo(pair), s) : 0u;
-                        const uint32_t w = s > 0.0f ? code_of(Act<DT>::hi(pair), s) : 0u;
-                        c0[j >> 2] = (c0[j >> 2] & keep) | u << (8 * (j & 3));
-                        c1[j >> 2] = (c1[j >> 2] & keep) | w << (8 * (j & 3));
+        for (int n = 0; n < N; ++n) {
+            const int lo = first + (n * NW * SPW + unit) * 16;
+            if (lo >= off + len || (!move && lo + 16 <= off))
+                continue;
+            int8_t *row0 = codes + (int64_t)d * block + lo, *row1 = row0 + block;
+            u32x4_t c0 = {0, 0, 0, 0}, c1 = {0, 0, 0, 0};
+            // codes before the run stay (at the new scale); places behind it
+            // are not live, and keep what they hold
+            if (lo < off || lo + 16 > off + len) {
+                c0 = *reinterpret_cast<const u32x4_t *>(row0);
+                c1 = *reinterpret_cast<const u32x4_t *>(row1);
+                if (move && lo < off) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const uint32_t live = low_bytes(off - lo - 4 * v);
+                        c0[v] = (c0[v] & ~live) | (rescaled4(c0[v], ratio) & live);
+                        c1[v] = (c1[v] & ~live) | (rescaled4(c1[v], ratio) & live);
                     }
                 }
-                *reinterpret_cast<u32x4_t *>(row0) = c0;
-                *reinterpret_cast<u32x4_t *>(row1) = c1;
             }
+            if (lo + 16 > off) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t u = 0, w = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        u |= code_of(Act<DT>::lo(raw[n][4 * v + j]), k) << (8 * j);
+                        w |= code_of(Act<DT>::hi(raw[n][4 * v + j]), k) << (8 * j);
+                    }
+                    const uint32_t fresh = low_bytes(off + len - lo - 4 * v) & ~low_bytes(off - lo - 4 * v);
+                    c0[v] = (c0[v] & ~fresh) | (u & fresh);
+                    c1[v] = (c1[v] & ~fresh) | (w & fresh);
+                }
+            }
+            *reinterpret_cast<u32x4_t *>(row0) = c0;
+            *reinterpret_cast<u32x4_t *>(row1) = c1;
         }
     }
 }
 
-// Grid: windows of WIN tokens, heads, keys and values.
-template <int DT, int D, int WIN>
+// Grid: windows of WIN tokens, heads, keys and values.  MOST: the block size,
+// or 64 for 32 and 64.  A run within one segment is a wave's work (in decode
+// every run is: a token), a longer one the workgroup's.
+template <int DT, int D, int WIN, int MOST>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCacheArgs a)
 {
-    __shared__ float lds[kThreads / 64];
+    __shared__ float lds[2][kThreads / 64];
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t t0 = (int64_t)blockIdx.x * WIN;
     const int head = blockIdx.y;
@@ -174,45 +223,62 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCacheArgs a)
     // A run begins where the slot before is not the one below, or at a block's
     // start.  Slots outside the cache (-1: padding) belong to no run.
     const int64_t mine = t0 + lane;
-    bool leads = false;
-    if (lane < WIN && mine < a.tokens) {
-        const int64_t s = a.slots[mine];
-        if (s >= 0 && s < n_slots)
-            leads = (s & (block - 1)) == 0 || mine == 0 || (int64_t)a.slots[mine - 1] + 1 != s;
-    }
-    uint64_t leaders = __ballot(leads);
-    const bool alone = __popcll(leaders) == 1;
-    for (int n = 0; leaders; ++n) {
-        const int l = __ffsll((unsigned long long)leaders) - 1;
-        leaders &= leaders - 1;
-        if (!alone && (n & 3) != wave)
-            continue;
-        const int64_t t = t0 + l;
-        const int64_t slot = a.slots[t];
-        const int off = (int)(slot & (block - 1)), most = block - off;
-        int len = 0;
-        for (int i = 0; i < most; i += 64) {
-            const int64_t at = t + i + lane;
-            const bool same = i + lane < most && at < a.tokens && (int64_t)a.slots[at] == slot + i + lane;
-            const uint64_t b = __ballot(same);
-            const int more = ~b ? __ffsll((unsigned long long)~b) - 1 : 64;
-            len += more;
-            if (more < 64)
-                break;
+    const bool here = lane < WIN && mine < a.tokens;
+    const int32_t s = here ? a.slots[mine] : -1;
+    const int32_t before = here && mine > 0 ? a.slots[mine - 1] : -2;
+    const bool live = s >= 0 && s < n_slots;
+    const bool leads = live && ((s & (block - 1)) == 0 || before != s - 1);
+    const uint64_t leaders = __ballot(leads), breaks = __ballot(leads || !live);
+
+    struct Run {
+        int64_t slot;
+        int off, len;
+        bool brief;
+    };
+    auto run_at = [&](int l) {
+        Run r;
+        r.slot = __builtin_amdgcn_readlane(s, l);
+        r.off = (int)(r.slot & (block - 1));
+        const uint64_t rest = l < 63 ? breaks >> (l + 1) : 0;
+        r.len = (rest ? __ffsll((unsigned long long)rest) : 64 - l);
+        if (l + r.len >= WIN) { // it may go on behind the window
+            const int most = block - r.off;
+            for (int i = r.len; i < most; i += 64) {
+                const int64_t at = t0 + l + i + lane;
+                const bool same = i + lane < most && at < a.tokens && (int64_t)a.slots[at] == r.slot + i + lane;
+                const uint64_t b = __ballot(same);
+                const int more = ~b ? __ffsll((unsigned long long)~b) - 1 : 64;
+                r.len += more;
+                if (more < 64)
+                    break;
+            }
         }
-        const int64_t blk = slot >> a.block_shift;
-        if (alone) {
-            if (blockIdx.z == 0)
-                write_run<DT, D, 4, false>(a, t, blk, off, len, head, wave, lds);
-            else
-                write_run<DT, D, 4, true>(a, t, blk, off, len, head, wave, lds);
-        } else {
-            if (blockIdx.z == 0)
-                write_run<DT, D, 1, false>(a, t, blk, off, len, head, 0, lds);
-            else
-                write_run<DT, D, 1, true>(a, t, blk, off, len, head, 0, lds);
-        }
+        r.brief = (r.off & 15) + r.len <= 16;
+        return r;
+    };
+    auto write = [&](auto waves, auto most, int l, const Run &r, int w, float *top) {
+        if (blockIdx.z == 0)
+            write_run<DT, D, decltype(waves)::value, decltype(most)::value, false>(a, t0 + l, r.slot >> a.block_shift, r.off, r.len,
+                                                                                    head, w, top);
+        else
+            write_run<DT, D, decltype(waves)::value, decltype(most)::value, true>(a, t0 + l, r.slot >> a.block_shift, r.off, r.len,
+                                                                                   head, w, top);
+    };
+    uint64_t longer = 0;
+    int n = 0;
+    for (uint64_t left = leaders; left; left &= left - 1) {
+        const int l = __ffsll((unsigned long long)left) - 1;
+        const Run r = run_at(l);
+        if (MOST > 16 && !r.brief)
+            longer |= uint64_t(1) << l;
+        else if ((n++ & 3) == wave)
+            write(Int<1>(), Int<16>(), l, r, 0, nullptr);
     }
+    if constexpr (MOST > 16)
+        for (n = 0; longer; longer &= longer - 1, ++n) {
+            const int l = __ffsll((unsigned long long)longer) - 1;
+            write(Int<kThreads / 64>(), Int<MOST>(), l, run_at(l), wave, lds[n & 1]);
+        }
 }
 
 // Read: 64 tokens of one head a workgroup.  Key rows are contiguous; the
@@ -272,16 +338,38 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCacheArgs a)
     }
 }
 
+template <int DT, int D, int WIN, int MOST>
+void write_window(const KvCacheArgs &a, hipStream_t stream)
+{
+    kv_write_kernel<DT, D, WIN, MOST><<<dim3((unsigned)((a.tokens + WIN - 1) / WIN), (unsigned)a.kv_heads, 2), dim3(kThreads), 0, stream>>>(a);
+}
+
+template <int DT, int D, int MOST>
+void write_block(const KvCacheArgs &a, hipStream_t stream)
+{
+    // Small windows suit single tokens, which a workgroup's waves take one after
+    // the other, large ones long runs, whose further windows hold nothing to do
+    // and cost a workgroup each.  With windows of 4, 16 and 64, us: 64 single
+    // tokens (2 heads of 128) 4.5, 10.6, 36, and 512 (8 heads) 14.7, 17.1, 41;
+    // 2048 (2 heads) 13.0, 15.0, 39, and one prompt of 2000 (8 heads, blocks of
+    // 16) 17.9, 6.3, 4.9; four prompts of 4000 (8 heads, blocks of 64) 166, 44, 26.
+    if (a.tokens <= 512)
+        write_window<DT, D, 4, MOST>(a, stream);
+    else if (a.tokens <= 4096)
+        write_window<DT, D, 16, MOST>(a, stream);
+    else
+        write_window<DT, D, 64, MOST>(a, stream);
+}
+
 template <int DT, int D>
 void write_dim(const KvCacheArgs &a, hipStream_t stream)
 {
-    // One token a workgroup while that keeps the number of workgroups low
-    // (runs are single tokens in decode, and each then has its own workgroup);
-    // windows of 16 for prompts, whose runs fill blocks of 16 or more.
-    if (a.tokens <= 2048)
-        kv_write_kernel<DT, D, 1><<<dim3((unsigned)a.tokens, (unsigned)a.kv_heads, 2), dim3(kThreads), 0, stream>>>(a);
+    if (a.block_shift == 4)
+        write_block<DT, D, 16>(a, stream);
+    else if (a.block_shift == 7)
+        write_block<DT, D, 128>(a, stream);
     else
-        kv_write_kernel<DT, D, 16><<<dim3((unsigned)((a.tokens + 15) / 16), (unsigned)a.kv_heads, 2), dim3(kThreads), 0, stream>>>(a);
+        write_block<DT, D, 64>(a, stream);
 }
 
 template <int DT, int D>
