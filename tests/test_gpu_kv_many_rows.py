@@ -1,6 +1,7 @@
 """kv_attention at sizes from which the call takes its kernel for many query
 rows (the other sizes are in test_gpu_kv.py), calls with more requests than a
-workgroup has threads, and a whole step in a replayed graph."""
+workgroup has threads, kv_write and qk_norm_rope with from few to many tokens
+a wave, and a whole step in a replayed graph."""
 
 import numpy as np
 import pytest
@@ -9,7 +10,7 @@ torch = pytest.importorskip("torch")
 import int8_weight_quantized_amd as qw  # noqa: E402
 import kv_reference as ref  # noqa: E402
 from gpu_util import say  # noqa: E402
-from test_gpu_kv import BF16, F16, TYPES, dev, host, ints, unit, within  # noqa: E402
+from test_gpu_kv import BF16, F16, TYPES, dev, host, ints, same, slots_of, unit, within, write_and_compare  # noqa: E402
 
 DIM = 128
 
@@ -267,6 +268,64 @@ def test_same_bits_and_streams():
     alone = qw.kv_attention(q[300:], *on, ints(table[1:]), ints(context[1:]), ints([0, 150]), 150)
     if many_rows(150, 1, 64, 8, 150):
         assert torch.equal(first[300:], alone)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("tokens,dim", [(511, 128), (512, 64), (513, 128), (2500, 64), (4096, 128), (4097, 64), (6000, 128)])
+def test_write_windows(tokens, dim, block, dtype):
+    """Windows of 4, 16 and 64 tokens over single tokens, short runs and long
+    ones, beginning and ending anywhere, with padding between requests."""
+    rng = np.random.default_rng(tokens + block)
+    fresh = []
+    while sum(fresh) < tokens:
+        n = int(rng.choice([1, 1, 1, 2, 7, 15, 16, 17, 40, 64, 130, 300]))
+        fresh.append(min(n, tokens - sum(fresh)))
+    past = [int(x) for x in rng.integers(0, 2 * block, len(fresh))]
+    context = [p + n for p, n in zip(past, fresh)]
+    table, blocks = ref.pages(rng, context, block)
+    slots = []
+    for r in range(len(fresh)):
+        slots += slots_of(table, r, past[r], context[r], block)
+    cut = int(np.cumsum(fresh)[len(fresh) // 2])
+    for at in (tokens, cut, 0):   # padding takes the place of tokens at the end
+        slots[at:at] = [-1, blocks * block, -7][:1 + at % 3]
+    write_and_compare(rng, slots, 2, dim, block, blocks, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,hq,hk,dim,rot,pairs,norm", [
+    (1, 70, 9, 64, 64, False, True), (2, 33, 1, 128, 128, True, True), (700, 5, 3, 128, 64, False, False),
+    (3000, 9, 2, 64, 64, False, True), (8192, 4, 1, 128, 96, True, True), (8300, 7, 2, 64, 32, False, True)])
+def test_norm_rope_waves(tokens, hq, hk, dim, rot, pairs, norm, dtype):
+    """From many waves a token to one for all of its heads; infinities in the
+    channels that do not turn, and in a row beside, stay where they are."""
+    rng = np.random.default_rng(tokens + dim + rot)
+    span = 64
+    say("norm_rope T=%d %d/%d D=%d rot=%d pairs=%s norm=%s %s" % (tokens, hq, hk, dim, rot, pairs, norm, dtype))
+    q, k = (dev(rng.standard_normal((tokens, h, dim)), dtype) for h in (hq, hk))
+    pos = rng.integers(-2, span + 1, tokens)
+    pos[0] = 5
+    angle = rng.uniform(0, 7, (span, rot // 2))
+    cos, sin = np.cos(angle).astype(np.float32), np.sin(angle).astype(np.float32)
+    wq, wk = (dev(1 + 0.3 * rng.standard_normal(dim), dtype) for _ in range(2)) if norm else (None, None)
+    args = (ints(pos), dev(cos), dev(sin), wq, wk)
+    got = qw.qk_norm_rope(q, k, *args, eps=1e-5, interleaved=pairs)
+    for g, x, w in zip(got, (q, k), (wq, wk)):
+        want, mag = ref.norm_rope(host(x), pos, cos, sin, None if w is None else host(w), 1e-5, pairs)
+        within(host(g), want, unit(dtype) * np.abs(want) + (dim + 8) * 2.0 ** -24 * mag + 2.0 ** -25)
+    bad = q.clone()
+    bad[0, 1, dim - 1] = float("inf")
+    other = qw.qk_norm_rope(bad, k, *args, eps=1e-5, interleaved=pairs)
+    a, b = host(got[0]), host(other[0])
+    same(b[0, 2:], a[0, 2:], "the heads beside")
+    same(b[1:], a[1:], "the tokens beside")
+    same(host(other[1]), host(got[1]), "the keys")
+    if not norm and rot < dim:
+        same(b[0, 1, :dim - 1], a[0, 1, :dim - 1], "the other channels")
+        assert np.isinf(b[0, 1, dim - 1])
 
 
 @pytest.mark.gpu
