@@ -14,13 +14,15 @@
 // down to 2^-29 of it), and P Vq with P rounded to fp16.
 //
 // The value scale is folded into the softmax's exponent:
-//   t_j = log2(e) s_j + log2 Sv(j),  P_j = 2^{t_j - M},  M >= max t_j - 8
+//   t_j = log2(e) s_j + log2 Sv(j),  P_j = 2^{t_j - M}
 //   o = sum P_j Vq[j] / sum (P_j / Sv(j))
-// so one running reference M serves both sums, P stays within 2^8 whatever
-// the scales of the blocks, and the denominator needs one multiplication per
-// 16 keys.  M moves only when a row's maximum has grown by 2^8 or more; the
-// accumulators are rescaled then.  M, the denominators and the accumulators
-// are fp32.
+// so one running reference M serves both sums, whatever the scales of the
+// blocks, and the denominator needs one multiplication per 16 keys.  M is
+// the maximum of the first tile in which the row sees a key, and moves to a
+// later tile's only where weights of that one add up to 2^15 (a sum that is
+// there anyway: no maximum is taken over the other tiles); the accumulators
+// are rescaled then.  So P stays below fp16's range, and some P is 1 or
+// more.  M, the denominators and the accumulators are fp32.
 //
 // Query rows that share a key head (the heads of its group, for each new
 // token) form the columns of one matrix product, so the cache is read once
@@ -33,7 +35,6 @@ namespace {
 
 constexpr int kThreads = 256; // of the join
 constexpr int kTile = 64; // keys a wave takes at once
-constexpr float kLazy = 8.0f;
 // What beginning and ending a unit costs a workgroup, in tiles: a workgroup
 // whose range spans several units is given fewer keys.  (0, 4 and 8: 34.3,
 // 32.9 and 33.4 us for 64 requests of 512 to 8192 keys, 38.0, 28.0 and 28.3 us
@@ -222,10 +223,12 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
     const int begin = p.begin > any_lo ? p.begin : any_lo, end = p.end < any_hi ? p.end : any_hi;
 
     float4_t o[RT][DTILES];
-    float m[RT], l[RT];
+    float m[RT], l[RT]; // the reference, and the denominator over this lane's keys
+    bool seen[RT];      // a key; the four lanes of a row agree
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        m[t] = -INFINITY;
+        m[t] = 0.0f;
+        seen[t] = p.row0 + t * 16 + col >= p.s.rows;
         l[t] = 0.0f;
 #pragma unroll
         for (int d = 0; d < DTILES; ++d)
@@ -291,41 +294,53 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
         half8_t w[RT][2];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const float c = ok ? mult[t] * ks : 0.0f;
-            float x[16];
-            float top = -INFINITY;
+            const float c = ok ? mult[t] * ks : 0.0f, b = lv - m[t];
+            float x[16], y[16], sum;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    x[4 * i + j] = fmaf(sc[t][i][j], c, lv);
+                    x[4 * i + j] = fmaf(sc[t][i][j], c, b);
             if (!whole) {
                 const int at = base + g * 16;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     x[e] = ok && at + e >= lim_lo[t] && at + e < lim_hi[t] ? x[e] : -INFINITY;
             }
+            auto weights = [&]() {
+                sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                top = fmaxf(top, x[e]);
-            top = max_xor32(max_xor16(top));
-            if (__any(top > m[t] + kLazy)) {
-                const float next = top > m[t] + kLazy ? top : m[t]; // (a row moves for its own sake only)
-                const float alpha = next == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - next);
-                m[t] = next;
+                for (int e = 0; e < 16; ++e) {
+                    y[e] = __builtin_amdgcn_exp2f(x[e]);
+                    sum += y[e];
+                }
+            };
+            weights();
+            if (__any(!seen[t] || sum >= kKvLarge)) {
+                // (a row moves for its own sake only: no result depends on which
+                // rows share a wave)
+                const float most = max_xor32(max_xor16(sum));
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    top = fmaxf(top, x[e]);
+                top = max_xor32(max_xor16(top));
+                const float up = seen[t] ? (most >= kKvLarge ? top : 0.0f) : (top > kKvNothing ? top : 0.0f);
+                const float alpha = seen[t] ? __builtin_amdgcn_exp2f(-up) : 1.0f;
+                m[t] += up;
+                seen[t] = seen[t] || top > kKvNothing;
                 l[t] *= alpha;
 #pragma unroll
                 for (int d = 0; d < DTILES; ++d)
                     o[t][d] *= alpha;
-            }
-            const float ref = m[t] == -INFINITY ? 0.0f : m[t];
-            float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float y = __builtin_amdgcn_exp2f(x[e] - ref);
-                sum += y;
-                w[t][e >> 3][e & 7] = (_Float16)y; // to nearest: 2^-11 of a weight at most
+                for (int e = 0; e < 16; ++e)
+                    x[e] -= up;
+                weights();
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                w[t][e >> 3][e & 7] = (_Float16)y[e]; // to nearest: 2^-11 of a weight at most
             l[t] = fmaf(sum, inv, l[t]);
         }
 #pragma unroll
@@ -345,7 +360,7 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
     for (int t = 0; t < RT; ++t) {
         l[t] = add_xor32(add_xor16(l[t]));
         if (g == 0) {
-            lds.m[wave][t * 16 + col] = m[t];
+            lds.m[wave][t * 16 + col] = seen[t] ? m[t] : -INFINITY;
             lds.l[wave][t * 16 + col] = l[t];
         }
 #pragma unroll

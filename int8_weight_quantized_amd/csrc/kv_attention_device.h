@@ -8,6 +8,10 @@
 
 namespace qw {
 
+// A row's reference moves where weights add up to kKvLarge: below it none
+// overflows fp16.  A maximum above kKvNothing is one of scores, not of masked places.
+constexpr float kKvLarge = 32768.0f, kKvNothing = -3e38f;
+
 __device__ __forceinline__ int kv_clamp(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
 // What one request asks for, bounded by what the arguments describe.

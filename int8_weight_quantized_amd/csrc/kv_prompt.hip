@@ -37,11 +37,9 @@ constexpr int kRows = 32 * kWaves; // query rows of a workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 64;
 constexpr int kSlots = 65; // of a fragment: a lane each, and one so that fragments begin at different banks
-constexpr float kLarge = 32768.0f; // of weights' sums: below it none overflows fp16
 constexpr int kAhead = 4; // fragments read ahead of the matrix instructions
 constexpr int kSegment = 64; // tiles whose scales are fetched at once
 constexpr int kFirst = 3; // number of the first tile: its buffers have index 0 (modulo 3)
-constexpr float kNothing = -3e38f; // the threshold of a row that has seen no key
 
 union PromptLds {
     struct {
@@ -304,7 +302,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
         };
         weights();
         float most = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
-        if (__any(!seen || most >= kLarge)) {
+        if (__any(!seen || most >= kKvLarge)) {
             // (a row moves for its own sake only: no result depends on which rows
             // share a wave)
             most = max_xor32(most);
@@ -315,10 +313,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
                 for (int i = 0; i < 16; ++i)
                     top = fmaxf(top, sc[t][i]);
             top = max_xor32(top);
-            const float up = seen ? (most >= kLarge ? top : 0.0f) : (top > kNothing ? top : 0.0f); // the new reference lies so far above the old
+            const float up = seen ? (most >= kKvLarge ? top : 0.0f) : (top > kKvNothing ? top : 0.0f); // the new reference lies so far above the old
             const float alpha = seen ? __builtin_amdgcn_exp2f(-up) : 1.0f;
             ref += up;
-            seen = seen || top > kNothing;
+            seen = seen || top > kKvNothing;
             l *= alpha;
 #pragma unroll
             for (int d = 0; d < DTILES; ++d)
