@@ -615,11 +615,11 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int uni
 // takes about 6 us for 32 rows in each of eight waves a CU, and shares any work
 // out evenly.  So up to 32 rows a key head, and where the row blocks leave too
 // many CUs idle, the split kernel runs.  Both, us, 32 query heads on 2 key
-// heads: one request of 512 tokens behind 8000 235 / 141, of 1024 alone 38 / 55,
-// 16 of up to 100 behind up to 3000 91 / 132, eight of up to 1024 71 / 108.
+// heads: one request of 512 tokens behind 8000 235 / 133, of 1024 alone 37 / 55,
+// 16 of up to 100 behind up to 3000 85 / 132, eight of up to 1024 67 / 108.
 // With 64 channels the split kernel was the faster everywhere from 40 tokens
-// to eight prompts of up to 4096 (an eight-wave prompt kernel: 264 / 268 there,
-// 47 / 34 for eight of up to 1024).
+// to eight prompts of up to 4096 (an eight-wave prompt kernel: 264 / 260 there,
+// 47 / 35 for eight of up to 1024).
 bool prompt_preferred(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t max_new)
 {
     if (max_new * group <= 32 || head_dim != 128)
@@ -650,7 +650,7 @@ SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int
     // One workgroup a unit where a unit is short, or where units fill the chip
     // some times over (then the dispatch balances them, also the unequal row
     // blocks of prompts, and nothing has to be joined: 1205 units of 65 tiles
-    // take 111 us so, and 191 and 30 for the join in ranges).
+    // take 90 us so; in ranges, an earlier form took 191 and 30 for the join).
     if (tiles <= 8 || all >= (int64_t(1) << 31) - (1 << 20) || requests * p.units >= 4 * (int64_t)p.groups)
         p.groups = 0;
     else if (all < kMinRange * (int64_t)p.groups)

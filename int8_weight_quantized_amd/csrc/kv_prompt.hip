@@ -12,17 +12,27 @@
 //
 // Tiles of 64 keys are cast to fp16 once, on their way into LDS, by all eight
 // waves (16 bytes of codes a thread and operand), and are read from there by
-// each wave in whole fragments of the matrix instruction: fragment f is 1 KiB,
-// 16 bytes a lane, lane l's piece in slot l ^ x with x the fragment's position
-// along the contiguous direction of the cache, so that both the reads (a
-// permutation of one KiB) and the writes (eight lanes hold consecutive pieces
-// of one row, that is eight fragments) touch all banks evenly.  Two buffers;
-// one barrier a tile.
+// each wave in whole fragments of the matrix instruction: fragment f is 64
+// pieces of 16 bytes, a lane's each, and a 65th place, so that the writes
+// (eight lanes hold consecutive pieces of one row, that is of eight
+// fragments) spread over the banks as the reads do.  Three buffers: the two
+// waves of a SIMD take turns, one in the matrix phase (the values of a tile,
+// the keys of the next) while the other is in the softmax phase, so that at
+// the same time one tile is read, the next is written and a third is still
+// read by the waves that come behind.  A barrier ends each phase.
 //
-// Bound by the matrix cores together with the softmax's VALU work: per tile
-// and wave 2 * D / 4 matrix instructions of 32 cycles, and for each of 32
-// scores a lane one FMA, half a maximum, one exponential at a quarter of the
-// rate, one addition and half a conversion.
+// Bound by the two phases' lengths: a matrix phase is 32 instructions of 32
+// cycles and takes some 1140 cycles; in the other, for each of 32 scores a
+// lane, one FMA, one exponential, one addition and half a conversion, which
+// at 5 cycles an instruction (9 an exponential) are as many.  The staging of
+// the next tile goes with the matrix phase (with the other one: 2 to 3 %
+// slower; dealt out among the matrix instructions by hand: 15 % slower).
+// Measured: four prompts of up to 8192 tokens, 32 query heads on 8 key heads,
+// causal: 1080 us, 970 TFLOP/s fp16, and 1050 us in bf16 with blocks of 16 (a
+// matrix product of 8192^3: 1151 and 1218); three of up to 4096 on 2 key heads
+// 290 us, 870 TFLOP/s, where the row blocks do not come out even over the CUs.
+// The form before this one (all waves in step, two buffers, staging with
+// branches) took 2147 us for the first.
 #include "kv_attention_device.h"
 
 namespace qw {
@@ -351,9 +361,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
     }
     __syncthreads();
 
-    // The two waves of a SIMD take turns: while waves 0 to 3 are in a matrix
-    // phase, waves 4 to 7 are in the softmax phase of the tile before, and the
-    // other way round.
+    // While waves 0 to 3 are in the softmax phase of a tile, waves 4 to 7 are in
+    // the matrix phase before it, and the other way round.  With a phase's number
+    // behind a barrier, the first waves' matrix phase of tile n is 2 n + 1, the
+    // others' 2 n + 2.  In it they put down the keys of tile n + 2 and the values
+    // of n + 1, which are read from phase 2 n + 3 on, in the place of keys n - 1
+    // and values n - 2, which were read in phase 2 n - 2 at the latest.
     const bool second = wave >= 4;
     if (second)
         __syncthreads();
@@ -363,11 +376,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
     int tile = kFirst;
     for (int base = begin; base < end; base += kTile, ++tile) {
         softmax(base);
-        stage(tile + 1, base + kTile);
         if (((tile - kFirst) & (kSegment - 1)) == kSegment / 2)
             segment_scales((tile - kFirst) / kSegment + 1);
         __syncthreads();
         __builtin_amdgcn_s_setprio(1);
+        stage(tile + 1, base + kTile);
         value_product(tile % 3);
         key_product((tile + 1) % 3); // (behind the last tile: not used)
         order();
