@@ -90,7 +90,8 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs &a, int r)
 // that lane group g = lane / 16 holds keys 16 g .. 16 g + 15 of the tile:
 // exactly the operand layout of the second product, whose other operand is
 // then one contiguous 16-byte load a lane from the transposed values.
-// Nothing passes through LDS or between lanes but the row maximum.
+// Nothing passes through LDS or between lanes until the unit's end, but a row's
+// maximum where its reference moves.
 //
 // Bound by HBM: 2 * D + 8 / B bytes a key and head, read straight into
 // registers; past the caches where there is one block of query rows (ONCE:
@@ -649,8 +650,9 @@ SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int
     p.groups = device_cu_count() * split_groups((int)head_dim, p.rt);
     // One workgroup a unit where a unit is short, or where units fill the chip
     // some times over (then the dispatch balances them, also the unequal row
-    // blocks of prompts, and nothing has to be joined: 1205 units of 65 tiles
-    // take 90 us so; in ranges, an earlier form took 191 and 30 for the join).
+    // blocks of prompts, and nothing has to be joined: 1264 units of up to 66
+    // tiles, 16 heads of 64, take 90 us so; in ranges an earlier form took 191,
+    // and 30 for the join, where it took 111 so).
     if (tiles <= 8 || all >= (int64_t(1) << 31) - (1 << 20) || requests * p.units >= 4 * (int64_t)p.groups)
         p.groups = 0;
     else if (all < kMinRange * (int64_t)p.groups)
