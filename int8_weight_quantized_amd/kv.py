@@ -281,8 +281,8 @@ def qk_norm_rope(q, k, positions, cos, sin, q_weight=None, k_weight=None, eps: f
         fine = False
     if fine:
         sq, sk, sqo, sko = sq[0], sk[0], hq * dim, hk * dim
-        qo = torch.empty((tokens, hq, dim), dtype=dtype, device=q.device)
-        ko = torch.empty((tokens, hk, dim), dtype=dtype, device=q.device)
+        # (strided views and heads in order: new tensors of their kind are contiguous)
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
     else:
         device = _pkg._require_gpu(q, "q")
         code, tokens, hq, hk, dim, rot, sq, sk, qo, sqo, ko, sko = _validate_norm_rope(
@@ -468,7 +468,7 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
     if fine:
         if scale is None:
             scale = 1.0 / math.sqrt(dim)
-        out = torch.empty_like(q) if q.is_contiguous() else torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
+        out = torch.empty_like(q)  # (contiguous, as in qk_norm_rope)
     else:
         device = _pkg._require_gpu(q, "q")
         code, tokens, heads, dim, sq, blocks, kv_heads, size, requests, width, max_context, scale, out = _validate_attention(
