@@ -17,11 +17,11 @@
 //   t_j = log2(e) s_j + log2 Sv(j),  P_j = 2^{t_j - M}
 //   o = sum P_j Vq[j] / sum (P_j / Sv(j))
 // so one running reference M serves both sums, whatever the scales of the
-// blocks, and the denominator needs one multiplication per 16 keys.  M is
-// the maximum of the first tile in which the row sees a key, and moves to a
-// later tile's only where weights of that one add up to 2^15 (a sum that is
+// blocks, and the denominator needs one multiplication per 16 keys.  M lies
+// 8 below the maximum of the first tile in which the row sees a key, and moves
+// to a later tile's only where weights of that one add up to 2^16 (a sum that is
 // there anyway: no maximum is taken over the other tiles); the accumulators
-// are rescaled then.  So P stays below fp16's range, and some P is 1 or
+// are rescaled then.  So P stays below fp16's range, and some P is 2^8 or
 // more.  M, the denominators and the accumulators are fp32.
 //
 // Query rows that share a key head (the heads of its group, for each new
@@ -326,7 +326,7 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
                 for (int e = 0; e < 16; ++e)
                     top = fmaxf(top, x[e]);
                 top = max_xor32(max_xor16(top));
-                const float up = seen[t] ? (most >= kKvLarge ? top : 0.0f) : (top > kKvNothing ? top : 0.0f);
+                const float up = (seen[t] ? most >= kKvLarge : top > kKvNothing) ? top - kKvRise : 0.0f;
                 const float alpha = seen[t] ? __builtin_amdgcn_exp2f(-up) : 1.0f;
                 m[t] += up;
                 seen[t] = seen[t] || top > kKvNothing;
@@ -341,7 +341,7 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                w[t][e >> 3][e & 7] = (_Float16)y[e]; // to nearest: 2^-11 of a weight at most
+                w[t][e >> 3][e & 7] = (_Float16)y[e]; // to nearest (the error: see kKvRise)
             l[t] = fmaf(sum, inv, l[t]);
         }
 #pragma unroll

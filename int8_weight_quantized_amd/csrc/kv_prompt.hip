@@ -323,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
                 for (int i = 0; i < 16; ++i)
                     top = fmaxf(top, sc[t][i]);
             top = max_xor32(top);
-            const float up = seen ? (most >= kKvLarge ? top : 0.0f) : (top > kKvNothing ? top : 0.0f); // the new reference lies so far above the old
+            const float up = (seen ? most >= kKvLarge : top > kKvNothing) ? top - kKvRise : 0.0f; // the new reference lies so far above the old
             const float alpha = seen ? __builtin_amdgcn_exp2f(-up) : 1.0f;
             ref += up;
             seen = seen || top > kKvNothing;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
             l = fmaf(sum[j], inv[j], l);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                p[j][e] = (_Float16)y[8 * j + e]; // to nearest: 2^-11 of a weight at most
+                p[j][e] = (_Float16)y[8 * j + e]; // to nearest (the error: see kKvRise)
         }
     };
 
