@@ -647,13 +647,17 @@ SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int
     if (window && window + max_new + kTile < span)
         span = window + max_new + kTile;
     const int64_t tiles = (span + kTile - 1) / kTile, all = (tiles + kUnitCost) * requests * p.units;
+    // What the device's sums can reach (in int32) whatever the lengths it finds:
+    // without a causal mask a window bounds no request's keys, if it has more
+    // queries than max_new.
+    const int64_t most = ((max_context + kTile - 1) / kTile + kUnitCost) * requests * p.units;
     p.groups = device_cu_count() * split_groups((int)head_dim, p.rt);
     // One workgroup a unit where a unit is short, or where units fill the chip
     // some times over (then the dispatch balances them, also the unequal row
     // blocks of prompts, and nothing has to be joined: 1264 units of up to 66
     // tiles, 16 heads of 64, take 90 us so; in ranges an earlier form took 191,
     // and 30 for the join, where it took 111 so).
-    if (tiles <= 8 || all >= (int64_t(1) << 31) - (1 << 20) || requests * p.units >= 4 * (int64_t)p.groups)
+    if (tiles <= 8 || most >= (int64_t(1) << 31) - (1 << 20) || requests * p.units >= 4 * (int64_t)p.groups)
         p.groups = 0;
     else if (all < kMinRange * (int64_t)p.groups)
         p.groups = (int)((all + kMinRange - 1) / kMinRange);
