@@ -62,7 +62,11 @@ enum Layout {
 // A request, with the keys that any of its rows sees and their cost.
 struct Request : KvRequest {
     int lo, hi; // keys; lo is a multiple of kTile
-    int cost;   // kTile-key tiles of that range, at least one, and kUnitCost; 0 without rows
+    int cost;   // of a unit: kTile-key tiles of that range, at least one, and kUnitCost; 0 without rows
+
+    // of all its units: those of each key head and block of 16 RT query rows
+    template <int RT>
+    __device__ __forceinline__ int total(const KvAttnArgs &a) const { return cost * ((rows + 16 * RT - 1) / (16 * RT) * a.kv_heads); }
 };
 
 __device__ __forceinline__ Request request_of(const KvAttnArgs &a, int r)
@@ -126,25 +130,36 @@ struct Piece {
     float *part;    // where it is left unfinished; null: it is the whole unit
 };
 
+// What the join has to know of a unit in several ranges.
+struct Cut {
+    int kvh, row0;
+    int first, last; // ranges that hold tiles of it
+    int slot;        // which of the first one's two pieces is its own
+    int t0, rows;
+};
+
 // A workgroup's range, handed out piece by piece.  The units of all requests
 // lie in a row, request by request, each as long as its cost: kUnitCost, then
 // its tiles.
 struct Range {
     int begin, at, stop;
-    Request s;   // request r; the requests before it cost `before` a unit
+    Request s;   // request r; the requests before it cost `before`
     int r, before;
     float *parts; // room for two pieces: one at the range's begin, one at its end
 
+    // `cut` (may be null) is told of the unit that begins here and goes on
+    // behind the range.
     template <int D, int RT>
-    __device__ __forceinline__ bool next(const KvAttnArgs &a, int units, Piece &p)
+    __device__ __forceinline__ bool next(const KvAttnArgs &a, Piece &p, Cut *cut)
     {
         while (at < stop) {
-            if (at >= (before + s.cost) * units) {
-                before += s.cost;
+            const int behind = before + s.template total<RT>(a);
+            if (at >= behind) {
+                before = behind;
                 s = request_of(a, ++r);
                 continue;
             }
-            const int rel = at - before * units;
+            const int rel = at - before;
             const int unit = rel / s.cost, from = rel - unit * s.cost;
             const int count = s.cost - from < stop - at ? s.cost - from : stop - at;
             const int off = from > kUnitCost ? from - kUnitCost : 0, tiles = from + count - kUnitCost - off;
@@ -155,10 +170,17 @@ struct Range {
             p.row0 = rb * 16 * RT;
             p.begin = s.lo + off * kTile;
             p.end = s.hi - p.begin < tiles * kTile ? s.hi : p.begin + tiles * kTile;
-            p.part = tiles == s.cost - kUnitCost ? nullptr : (at == begin ? parts : parts + piece_floats(D, RT));
+            const bool leads = at == begin;
+            p.part = tiles == s.cost - kUnitCost ? nullptr : (leads ? parts : parts + piece_floats(D, RT));
             at += count;
-            if (tiles > 0 && p.row0 < s.rows)
+            if (tiles > 0) {
+                if (p.part && off == 0 && cut) { // (so this is not the last range, and as long as all but that)
+                    const int last = (before + (unit + 1) * s.cost - 1) / (stop - begin);
+                    if (threadIdx.x == 0)
+                        *cut = {p.kvh, p.row0, (int)blockIdx.x, last, leads ? 0 : 1, s.t0, s.rows};
+                }
                 return true;
+            }
         }
         return false;
     }
@@ -418,7 +440,7 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
 // One workgroup a unit: for contexts that one workgroup reads fast enough,
 // or units enough to fill the chip many times over.
 template <int D, int RT, int DT, int LAYOUT, bool ONCE>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a, int units)
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a)
 {
     __shared__ __attribute__((aligned(16))) SplitLds<D, RT> lds;
     const Request s = request_of(a, blockIdx.y);
@@ -429,18 +451,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a, i
 }
 
 // The tiles of all units in a row, cut into equal ranges, split_groups a CU:
-// every workgroup streams the same number of keys, whatever the lengths of
-// the requests and however far the host's bound is above them.  A unit that lies
-// in one range is written out; the others' pieces (a range has two at most:
-// where it begins and where it ends) go to the workspace and are joined by a
-// second kernel.
+// every workgroup streams the same number of keys, whatever the requests' numbers
+// of keys and of query rows and however far the host's bounds are above them.  A
+// unit that lies in one range is written out; the others' pieces (a range has
+// two at most: where it begins and where it ends) go to the workspace and are
+// joined by a second kernel.
 //
-// Workspace: int32 cost of a range; int32 cost before each request, per unit
-// (requests + 1 of them); from the next multiple of four words on, two pieces a range.
-__device__ __host__ __forceinline__ int64_t parts_offset(int64_t requests) { return (requests + 2 + 3) / 4 * 4; }
+// Workspace: the ranges' length and the cost before each request (int32,
+// requests + 1 of them) for a join by requests, or a Cut a range for a join by
+// ranges; from the next multiple of four words on, two pieces a range.
+__device__ __host__ __forceinline__ int64_t parts_offset(int64_t requests, int64_t groups)
+{
+    const int64_t cuts = groups * (int64_t)(sizeof(Cut) / sizeof(int32_t));
+    return ((cuts > requests + 1 ? cuts : requests + 1) + 3) / 4 * 4;
+}
 
 template <int D, int RT, int DT, int LAYOUT, bool ONCE>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a, int units)
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a, bool by_ranges)
 {
     constexpr int NW = kWaves, NT = 64 * NW;
     __shared__ __attribute__((aligned(16))) SplitLds<D, RT> lds;
@@ -449,6 +476,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
     __shared__ int found_r, found_before; // its number and the cost before it
     const int lane = __lane_id(), wave = (int)threadIdx.x >> 6;
     int32_t *head = reinterpret_cast<int32_t *>(a.workspace);
+    Cut *cuts = reinterpret_cast<Cut *>(a.workspace);
 
     // Cost before each request of a batch of NT; `sum` grows by the batch's.
     auto scan = [&](int cost, int &sum) {
@@ -482,33 +510,32 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
             __syncthreads(); // wave_sums has been read
         const int r = base + (int)threadIdx.x;
         mine = batch(r);
-        before = scan(mine.cost, total);
-        if (blockIdx.x == 0 && r < a.requests)
+        before = scan(mine.template total<RT>(a), total);
+        if (!by_ranges && blockIdx.x == 0 && r < a.requests)
             head[1 + r] = before;
     }
-    const int all = total * units;
-    int per = (all + (int)gridDim.x - 1) / (int)gridDim.x;
+    int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     per = per < kMinRange ? kMinRange : per;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (by_ranges && threadIdx.x == 0)
+        cuts[blockIdx.x] = {0, 0, 0, -1, 0, 0, 0};
+    if (!by_ranges && blockIdx.x == 0 && threadIdx.x == 0)
         head[0] = per;
-        head[1 + a.requests] = total;
-    }
     Range range;
     range.begin = range.at = (int)blockIdx.x * per;
-    if (range.at >= all)
+    if (range.at >= total)
         return;
-    range.stop = all - range.at < per ? all : range.at + per;
-    range.parts = a.workspace + parts_offset(a.requests) + (int64_t)blockIdx.x * 2 * piece_floats(D, RT);
-    const int first = range.at / units;
+    range.stop = total - range.at < per ? total : range.at + per;
+    range.parts = a.workspace + parts_offset(a.requests, gridDim.x) + (int64_t)blockIdx.x * 2 * piece_floats(D, RT);
+    const int first = range.at;
     int sum = 0;
     for (int base = 0; base < a.requests; base += NT) {
         const int r = base + (int)threadIdx.x;
         if (a.requests > NT) { // once more, batch by batch
             __syncthreads();
             mine = batch(r);
-            before = scan(mine.cost, sum);
+            before = scan(mine.template total<RT>(a), sum);
         }
-        if (before <= first && first < before + mine.cost) {
+        if (before <= first && first < before + mine.template total<RT>(a)) {
             found = mine;
             found_r = r;
             found_before = before;
@@ -527,39 +554,51 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
     range.s.hi = __builtin_amdgcn_readfirstlane(found.hi);
     range.s.cost = __builtin_amdgcn_readfirstlane(found.cost);
     Piece p;
-    while (range.template next<D, RT>(a, units, p))
+    while (range.template next<D, RT>(a, p, by_ranges ? cuts + blockIdx.x : nullptr))
         split_piece<D, RT, DT, LAYOUT, ONCE>(a, p, lds);
 }
 
-// Joins the pieces of a row: one workgroup a row, its four waves over the
-// pieces, their lanes over the channels.
-template <int D, int RT, int DT>
-__global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int units)
+// Joins the pieces of a row: a workgroup for each row, its four waves over the
+// pieces, their lanes over the channels.  By requests (the grid is rows, key
+// heads, requests), or where these are too many, most of them empty because
+// the requests' numbers of rows differ, by ranges (those, and the rows of a unit),
+// the unit that is cut at the range's end being the workgroup's.
+template <int D, int RT, int DT, bool BY_RANGES>
+__global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int groups)
 {
     constexpr int E = D / 64;
     __shared__ float lds[4][64 * E + 2];
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int row = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
-    const int32_t *head = reinterpret_cast<const int32_t *>(a.workspace);
-    const int per = head[0], before = head[1 + r], cost = head[2 + r] - before;
-    const Request s = request_of(a, r);
-    if (row >= s.rows)
-        return;
-    const int rb = row / (16 * RT), unit = rb * a.kv_heads + kvh;
-    const int at = before * units + unit * cost; // where the unit begins
-    const int first = (at + kUnitCost) / per, last = (at + cost - 1) / per; // the ranges that hold tiles of it
-    if (first == last)
-        return; // written by its only workgroup
+    Cut cut;
+    int row;
+    if (BY_RANGES) {
+        cut = reinterpret_cast<const Cut *>(a.workspace)[blockIdx.x];
+        row = cut.row0 + (int)blockIdx.y;
+        if (cut.last < 0 || row >= cut.rows)
+            return;
+    } else {
+        const int32_t *head = reinterpret_cast<const int32_t *>(a.workspace);
+        const int r = blockIdx.z, per = head[0], before = head[1 + r];
+        const Request s = request_of(a, r);
+        row = blockIdx.x;
+        if (row >= s.rows)
+            return;
+        const int rb = row / (16 * RT), at = before + (rb * a.kv_heads + (int)blockIdx.y) * s.cost; // where the unit begins
+        cut = {(int)blockIdx.y, rb * 16 * RT, (at + kUnitCost) / per, (at + s.cost - 1) / per, 0, s.t0, s.rows};
+        if (cut.first == cut.last)
+            return; // written by its only workgroup
+        cut.slot = at > cut.first * per; // behind the end of another unit, else first in its range
+    }
+    const int first = cut.first;
     constexpr int64_t piece = piece_floats(D, RT);
-    const float *parts = a.workspace + parts_offset(a.requests) + (row - rb * 16 * RT) * (D + 4);
-    // the unit begins a range, or lies behind the end of another
-    auto part_of = [&](int w) { return parts + ((int64_t)w * 2 + (w == first && at > first * per ? 1 : 0)) * piece; };
+    const float *parts = a.workspace + parts_offset(a.requests, groups) + (row - cut.row0) * (D + 4);
+    auto part_of = [&](int w) { return parts + ((int64_t)w * 2 + (w == first ? cut.slot : 0)) * piece; };
     float m = -INFINITY, l = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         acc[e] = 0.0f;
 #pragma unroll 4
-    for (int w = first + wave; w <= last; w += 4) {
+    for (int w = first + wave; w <= cut.last; w += 4) {
         const float *p = part_of(w);
         const float pm = p[D], pl = p[D + 1];
         float v[E];
@@ -603,8 +642,8 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int uni
             acc[e] += lds[w][lane * E + e] * f;
     }
     const float n = l == 0.0f ? 0.0f : 1.0f / l;
-    const int i = row / a.group, qh = kvh * a.group + row - i * a.group;
-    uint16_t *out = a.out + ((int64_t)(s.t0 + i) * a.q_heads + qh) * D + lane * E;
+    const int i = row / a.group, qh = cut.kvh * a.group + row - i * a.group;
+    uint16_t *out = a.out + ((int64_t)(cut.t0 + i) * a.q_heads + qh) * D + lane * E;
     if (E == 2)
         *reinterpret_cast<uint32_t *>(out) = Act<DT>::pack(acc[0] * n, acc[E - 1] * n);
     else
@@ -668,15 +707,21 @@ template <int D, int RT, int DT, int LAYOUT, bool ONCE>
 hipError_t launch_split(const KvAttnArgs &a, const SplitShape &p, hipStream_t stream)
 {
     if (p.groups == 0) {
-        kv_unit_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.units, (unsigned)a.requests), dim3(64 * kWaves), 0, stream>>>(a, p.units);
+        kv_unit_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.units, (unsigned)a.requests), dim3(64 * kWaves), 0, stream>>>(a);
         return hipGetLastError();
     }
-    kv_stream_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.groups), dim3(64 * kWaves), 0, stream>>>(a, p.units);
+    const int rows = a.max_new * a.group, most = rows < 16 * RT ? rows : 16 * RT; // of a key head, and of a unit
+    // The join that has fewer workgroups.  (By ranges always: 83 us for 79 for two
+    // requests of five tokens, 32 heads on 8.)
+    const bool by_ranges = (int64_t)rows * a.kv_heads * a.requests > (int64_t)p.groups * most;
+    kv_stream_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.groups), dim3(64 * kWaves), 0, stream>>>(a, by_ranges);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    kv_join_kernel<D, RT, DT><<<dim3((unsigned)(a.max_new * a.group), (unsigned)a.kv_heads, (unsigned)a.requests),
-                                dim3(kThreads), 0, stream>>>(a, p.units);
+    if (by_ranges)
+        kv_join_kernel<D, RT, DT, true><<<dim3((unsigned)p.groups, (unsigned)most), dim3(kThreads), 0, stream>>>(a, p.groups);
+    else
+        kv_join_kernel<D, RT, DT, false><<<dim3((unsigned)rows, (unsigned)a.kv_heads, (unsigned)a.requests), dim3(kThreads), 0, stream>>>(a, p.groups);
     return hipGetLastError();
 }
 
@@ -708,7 +753,7 @@ int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads
     const SplitShape p = split_shape(requests, kv_heads, head_dim, q_heads / kv_heads, max_new, max_context, window);
     if (p.groups == 0)
         return 0;
-    return (parts_offset(requests) + (int64_t)p.groups * 2 * piece_floats((int)head_dim, p.rt)) * (int64_t)sizeof(float);
+    return (parts_offset(requests, p.groups) + (int64_t)p.groups * 2 * piece_floats((int)head_dim, p.rt)) * (int64_t)sizeof(float);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, int dtype, hipStream_t stream)
