@@ -44,6 +44,14 @@ constexpr int kMinRange = 4 + kUnitCost; // of a workgroup's range, at least
 
 constexpr int kWaves = 4; // of a split workgroup
 
+// Tiles in one workgroup that are worth two more launches (see attn_plan): some
+// 70 us of the prompt kernel, at 2.3 a tile, or of the split kernel, at 0.5.
+// There a quarter of that where most workgroups find no rows: they pass through
+// what slots the long ones leave (64 requests, one of 512 tokens and the others
+// of one behind 8000: 451 us and 86).  (32 always: eight windowed chunks of 64
+// channels, up to 72 tiles and half of the workgroups empty, 96 us for 91.)
+constexpr int long_walk(bool prompt, bool sparse) { return prompt || sparse ? 32 : 128; }
+
 // Ranges a CU.  Two keep its memory pipe full where a tile is 16 KiB; with
 // tiles of 8 KiB and one row tile three do better (24.9 us against 28.0 for
 // 48 requests of 128 to 2048 keys, 16 key heads of 64 channels), while at 128
@@ -457,13 +465,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a)
 // two at most: where it begins and where it ends) go to the workspace and are
 // joined by a second kernel.
 //
-// Workspace: the ranges' length and the cost before each request (int32,
-// requests + 1 of them) for a join by requests, or a Cut a range for a join by
-// ranges; from the next multiple of four words on, two pieces a range.
+// Workspace: for a join by requests the ranges' length, the cost before each
+// request and that of its units (int32, 2 requests + 1 of them), for a join by
+// ranges a Cut a range; from the next multiple of four words on, two pieces a
+// range.
 __device__ __host__ __forceinline__ int64_t parts_offset(int64_t requests, int64_t groups)
 {
     const int64_t cuts = groups * (int64_t)(sizeof(Cut) / sizeof(int32_t));
-    return ((cuts > requests + 1 ? cuts : requests + 1) + 3) / 4 * 4;
+    return ((cuts > 2 * requests + 1 ? cuts : 2 * requests + 1) + 3) / 4 * 4;
 }
 
 template <int D, int RT, int DT, int LAYOUT, bool ONCE>
@@ -511,8 +520,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
         const int r = base + (int)threadIdx.x;
         mine = batch(r);
         before = scan(mine.template total<RT>(a), total);
-        if (!by_ranges && blockIdx.x == 0 && r < a.requests)
-            head[1 + r] = before;
+        if (!by_ranges && blockIdx.x == 0 && r < a.requests) {
+            head[1 + 2 * r] = before;
+            head[2 + 2 * r] = mine.cost;
+        }
     }
     int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     per = per < kMinRange ? kMinRange : per;
@@ -578,13 +589,13 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int gro
             return;
     } else {
         const int32_t *head = reinterpret_cast<const int32_t *>(a.workspace);
-        const int r = blockIdx.z, per = head[0], before = head[1 + r];
-        const Request s = request_of(a, r);
+        const int r = blockIdx.z, per = head[0], before = head[1 + 2 * r], cost = head[2 + 2 * r];
+        const KvRequest s = kv_request(a, r);
         row = blockIdx.x;
         if (row >= s.rows)
             return;
-        const int rb = row / (16 * RT), at = before + (rb * a.kv_heads + (int)blockIdx.y) * s.cost; // where the unit begins
-        cut = {(int)blockIdx.y, rb * 16 * RT, (at + kUnitCost) / per, (at + s.cost - 1) / per, 0, s.t0, s.rows};
+        const int rb = row / (16 * RT), at = before + (rb * a.kv_heads + (int)blockIdx.y) * cost; // where the unit begins
+        cut = {(int)blockIdx.y, rb * 16 * RT, (at + kUnitCost) / per, (at + cost - 1) / per, 0, s.t0, s.rows};
         if (cut.first == cut.last)
             return; // written by its only workgroup
         cut.slot = at > cut.first * per; // behind the end of another unit, else first in its range
@@ -650,6 +661,15 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttnArgs a, int gro
         *out = (uint16_t)Act<DT>::pack(acc[0] * n, 0.0f);
 }
 
+// Tiles that a row's workgroup may have to go through.
+int64_t longest_walk(int64_t max_new, int64_t max_context, int64_t window)
+{
+    int64_t span = max_context;
+    if (window && window + max_new + kTile < span)
+        span = window + max_new + kTile;
+    return (span + kTile - 1) / kTile;
+}
+
 // Whether the prompt kernel is the faster one (it takes 128 channels).  Its
 // workgroups of 256 rows take 2.3 us for 64 keys, one a CU; the split kernel
 // takes about 6 us for 32 rows in each of eight waves a CU, and shares any work
@@ -675,17 +695,14 @@ struct SplitShape {
     int groups; // workgroups of the streamed form; 0: one a unit
 };
 
-SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t max_new, int64_t max_context,
+// `rows`: the most query rows of a key head.
+SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t rows, int64_t max_new, int64_t max_context,
                        int64_t window)
 {
     SplitShape p;
-    const int64_t rows = max_new * group;
     p.rt = rows <= 16 ? 1 : 2;
     p.units = (int)((rows + 16 * p.rt - 1) / (16 * p.rt) * kv_heads);
-    int64_t span = max_context;
-    if (window && window + max_new + kTile < span)
-        span = window + max_new + kTile;
-    const int64_t tiles = (span + kTile - 1) / kTile, all = (tiles + kUnitCost) * requests * p.units;
+    const int64_t tiles = longest_walk(max_new, max_context, window), all = (tiles + kUnitCost) * requests * p.units;
     // What the device's sums can reach (in int32) whatever the lengths it finds:
     // without a causal mask a window bounds no request's keys, if it has more
     // queries than max_new.
@@ -695,11 +712,50 @@ SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int
     // some times over (then the dispatch balances them, also the unequal row
     // blocks of prompts, and nothing has to be joined: 1264 units of up to 66
     // tiles, 16 heads of 64, take 90 us so; in ranges an earlier form took 191,
-    // and 30 for the join, where it took 111 so).
-    if (tiles <= 8 || most >= (int64_t(1) << 31) - (1 << 20) || requests * p.units >= 4 * (int64_t)p.groups)
+    // and 30 for the join, where it took 111 so).  With a block of rows a request,
+    // not if contexts may be long: a single long one among them would be one
+    // workgroup's work (192 tokens behind 1000, 16 heads of 64: 58 us so, 67 in
+    // ranges, but 686 and 113 if one of them stands behind 131072; all behind 4000
+    // 237 and 244, behind 8000 473 and 481).
+    const bool fill = requests * p.units >= 4 * (int64_t)p.groups && (p.units > kv_heads || tiles <= 64);
+    if (tiles <= 8 || most >= (int64_t(1) << 31) - (1 << 20) || fill)
         p.groups = 0;
     else if (all < kMinRange * (int64_t)p.groups)
         p.groups = (int)((all + kMinRange - 1) / kMinRange);
+    return p;
+}
+
+// What a call launches.
+struct AttnPlan {
+    bool prompt;      // the prompt kernel, else the split kernel of shape `main`,
+    int main_least;   // for the requests with at least so many rows a key head,
+    SplitShape main;
+    bool rest;        // and the split kernel of shape `few` for the others
+    SplitShape few;
+};
+
+AttnPlan attn_plan(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t max_new,
+                   int64_t max_context, int64_t window)
+{
+    AttnPlan p = {};
+    p.prompt = prompt_preferred(tokens, requests, kv_heads, head_dim, group, max_new);
+    p.main = split_shape(requests, kv_heads, head_dim, max_new * group, max_new, max_context, window);
+    // The prompt kernel, and the split kernel with a workgroup a unit, give all
+    // the keys of a row block to one workgroup.  Where a request may have few rows
+    // (some have fewer than max_new tokens) behind more keys than prompts have,
+    // those with one row block go to the split kernel in ranges.  Us, before and
+    // after, 32 heads on 2: a prompt of 4096 and a token behind 131072 3336 / 191, one
+    // of 2048 and 63 tokens behind 8000 250 / 127, of 512 and those 451 / 86; eight
+    // chunks of up to 512 behind 15000, which gain nothing, 570 / 570.
+    const int64_t few_new = group < 32 ? 32 / group : 1;
+    const bool serial = p.prompt || p.main.groups == 0;
+    const bool sparse = requests * p.main.units > 2 * (tokens * group / (16 * p.main.rt) + requests) * kv_heads;
+    if (serial && max_new > few_new && tokens < requests * max_new &&
+        longest_walk(max_new, max_context, window) >= (max_new + kTile - 1) / kTile + long_walk(p.prompt, sparse)) {
+        p.few = split_shape(requests, kv_heads, head_dim, few_new * group, few_new, max_context, window);
+        p.rest = p.few.groups > 0;
+        p.main_least = p.rest ? (int)(few_new * group) + 1 : 0;
+    }
     return p;
 }
 
@@ -710,7 +766,8 @@ hipError_t launch_split(const KvAttnArgs &a, const SplitShape &p, hipStream_t st
         kv_unit_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.units, (unsigned)a.requests), dim3(64 * kWaves), 0, stream>>>(a);
         return hipGetLastError();
     }
-    const int rows = a.max_new * a.group, most = rows < 16 * RT ? rows : 16 * RT; // of a key head, and of a unit
+    const int bound = a.max_new * a.group, rows = bound < a.most_rows ? bound : a.most_rows; // of a key head
+    const int most = rows < 16 * RT ? rows : 16 * RT;                                      // of a unit
     // The join that has fewer workgroups.  (By ranges always: 83 us for 79 for two
     // requests of five tokens, 32 heads on 8.)
     const bool by_ranges = (int64_t)rows * a.kv_heads * a.requests > (int64_t)p.groups * most;
@@ -735,9 +792,8 @@ hipError_t launch_layout(const KvAttnArgs &a, const SplitShape &p, hipStream_t s
 }
 
 template <int D, int DT>
-hipError_t launch_dim(const KvAttnArgs &a, hipStream_t stream)
+hipError_t launch_dim(const KvAttnArgs &a, const SplitShape &p, hipStream_t stream)
 {
-    const SplitShape p = split_shape(a.requests, a.kv_heads, D, a.group, a.max_new, a.max_context, a.window);
     if (p.rt == 1)
         return launch_layout<D, 1, DT, true>(a, p, stream);
     return p.units == a.kv_heads ? launch_layout<D, 2, DT, true>(a, p, stream) : launch_layout<D, 2, DT, false>(a, p, stream);
@@ -748,23 +804,39 @@ hipError_t launch_dim(const KvAttnArgs &a, hipStream_t stream)
 int64_t kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                int64_t requests, int64_t max_new, int64_t max_context, int64_t window)
 {
-    if (prompt_preferred(tokens, requests, kv_heads, head_dim, q_heads / kv_heads, max_new))
-        return 0;
-    const SplitShape p = split_shape(requests, kv_heads, head_dim, q_heads / kv_heads, max_new, max_context, window);
-    if (p.groups == 0)
-        return 0;
-    return (parts_offset(requests, p.groups) + (int64_t)p.groups * 2 * piece_floats((int)head_dim, p.rt)) * (int64_t)sizeof(float);
+    const AttnPlan p = attn_plan(tokens, requests, kv_heads, head_dim, q_heads / kv_heads, max_new, max_context, window);
+    auto bytes = [&](const SplitShape &f) {
+        return (parts_offset(requests, f.groups) + (int64_t)f.groups * 2 * piece_floats((int)head_dim, f.rt)) * (int64_t)sizeof(float);
+    };
+    if (p.rest)
+        return bytes(p.few); // (nothing is left to join by the others)
+    return p.prompt || p.main.groups == 0 ? 0 : bytes(p.main);
 }
+
+namespace {
+
+hipError_t launch_split_any(const KvAttnArgs &a, const SplitShape &p, int dtype, hipStream_t stream)
+{
+    if (a.head_dim == 64)
+        return dtype == QW_F16 ? launch_dim<64, QW_F16>(a, p, stream) : launch_dim<64, QW_BF16>(a, p, stream);
+    if (a.head_dim == 128)
+        return dtype == QW_F16 ? launch_dim<128, QW_F16>(a, p, stream) : launch_dim<128, QW_BF16>(a, p, stream);
+    return hipErrorInvalidValue;
+}
+
+} // namespace
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, int dtype, hipStream_t stream)
 {
-    if (prompt_preferred(a.tokens, a.requests, a.kv_heads, a.head_dim, a.group, a.max_new))
-        return launch_kv_prompt(a, dtype, stream);
-    if (a.head_dim == 64)
-        return dtype == QW_F16 ? launch_dim<64, QW_F16>(a, stream) : launch_dim<64, QW_BF16>(a, stream);
-    if (a.head_dim == 128)
-        return dtype == QW_F16 ? launch_dim<128, QW_F16>(a, stream) : launch_dim<128, QW_BF16>(a, stream);
-    return hipErrorInvalidValue;
+    const AttnPlan p = attn_plan(a.tokens, a.requests, a.kv_heads, a.head_dim, a.group, a.max_new, a.max_context, a.window);
+    KvAttnArgs part = a;
+    part.least_rows = p.main_least;
+    const hipError_t e = p.prompt ? launch_kv_prompt(part, dtype, stream) : launch_split_any(part, p.main, dtype, stream);
+    if (e != hipSuccess || !p.rest)
+        return e;
+    part.least_rows = 0;
+    part.most_rows = p.main_least - 1;
+    return launch_split_any(part, p.few, dtype, stream);
 }
 
 } // namespace qw

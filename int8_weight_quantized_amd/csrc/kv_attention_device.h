@@ -27,7 +27,7 @@ __device__ __forceinline__ int kv_clamp(int v, int lo, int hi) { return v < lo ?
 struct KvRequest {
     int t0, past; // first token; cached tokens before it (negative where there are more queries than cached tokens)
     int ctx;      // cached tokens
-    int rows;     // query rows of a key head: those of at most max_new tokens
+    int rows;     // query rows of a key head: those of at most max_new tokens; 0 if the launch does not take them
 };
 
 __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs &a, int r)
@@ -37,7 +37,8 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs &a, int r)
     const int n = kv_clamp(a.cu_tokens[r + 1], s.t0, a.tokens) - s.t0;
     s.ctx = kv_clamp(a.context[r], 0, a.max_context);
     s.past = s.ctx - n;
-    s.rows = (n < a.max_new ? n : a.max_new) * a.group;
+    const int rows = (n < a.max_new ? n : a.max_new) * a.group;
+    s.rows = rows >= a.least_rows && rows <= a.most_rows ? rows : 0;
     return s;
 }
 

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 import int8_weight_quantized_amd as qw  # noqa: E402
 from gpu_util import say  # noqa: E402
-from test_gpu_kv import F16, TYPES, ints  # noqa: E402
+from test_gpu_kv import BF16, F16, TYPES, ints  # noqa: E402
 from test_gpu_kv_many_rows import compare  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -40,8 +40,9 @@ def filled(blocks, kv, dim, block):
 
 def call_of(new, context, heads, kv, dim, block, max_new=None):
     width = -(-max(context) // block)
-    cache = filled(len(new) * width, kv, dim, block)
-    table = torch.arange(len(new) * width, dtype=torch.int32, device="cuda:0").view(len(new), width)
+    blocks = min(len(new) * width, (2 ** 32 if dim == 128 else 2 ** 31) // (kv * dim * block))   # (shared, if there are too many)
+    cache = filled(blocks, kv, dim, block)
+    table = (torch.arange(len(new) * width, dtype=torch.int32, device="cuda:0") % blocks).view(len(new), width)
     q = torch.randn((sum(new), heads, dim), device="cuda:0").to(F16)
     args = (q, *cache, table, ints(context), ints(np.concatenate([[0], np.cumsum(new)])), max_new or max(new))
     return lambda: qw.kv_attention(*args)
@@ -77,3 +78,45 @@ def test_one_draft_beside_decodes_takes_no_multiple_of_the_time():
     loose = microseconds(call_of([1] * 64, context, 32, 2, 128, 64, max_new=8))
     print("decodes %.1f us, with a draft %.1f us, with a loose bound %.1f us" % (alone, mixed, loose))
     assert mixed < 2 * alone and loose < 2 * alone
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 4000), (False, 4000), (True, 50)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompts_beside_tokens_behind_long_contexts(dtype, causal, window):
+    """Requests with few rows and with many in one call: up to 4 new tokens of 8
+    heads a key head go one way, more of them the other."""
+    rng = np.random.default_rng(window)
+    new, past = [450, 1, 3, 0, 200, 1, 4, 5, 1], [0, 5000, 4100, 77, 30, 0, 6000, 4500, 2]
+    compare(rng, new, [n + p for n, p in zip(new, past)], 64, 8, 32, dtype, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("heads,kv,dim,tokens", [(16, 16, 64, 2100), (40, 1, 64, 1800), (64, 1, 128, 300), (48, 16, 128, 700)])
+def test_groups_of_heads_beside_long_contexts(heads, kv, dim, tokens):
+    rng = np.random.default_rng(heads)
+    few = max(1, 32 // (heads // kv))
+    new = [tokens, 1, few, few + 1, 0, 1]
+    past = [5, tokens + 3000, tokens + 2500, tokens + 2600, 9, 40]
+    compare(rng, new, [n + p for n, p in zip(new, past)], heads, kv, 16, BF16, dim=dim, prompt=False)
+
+
+@pytest.mark.parametrize("requests,heads,kv,dim", [(200, 16, 16, 64), (1100, 4, 2, 128)])
+def test_many_tokens_and_one_long_context(requests, heads, kv, dim):
+    rng = np.random.default_rng(requests)
+    context = [int(c) for c in rng.integers(0, 60, requests)]
+    context[7], context[requests // 2] = 9000, 4500
+    compare(rng, [1] * requests, context, heads, kv, 64, F16, dim=dim, prompt=False)
+
+
+@pytest.mark.parametrize("what,heads,kv,dim,first,second", [
+    ("a prompt beside one token", 32, 2, 128, ([4096], [4096]), ([1], [131072])),
+    ("a prompt beside 63 tokens", 32, 2, 128, ([512], [512]), ([1] * 63, [8000] * 63)),
+    ("a prompt beside one token, 64 channels", 16, 16, 64, ([4096], [4096]), ([1], [131072])),
+    ("192 tokens, one far behind", 16, 16, 64, ([1] * 191, [1000] * 191), ([1], [131072])),
+])
+def test_a_long_context_is_shared_out(what, heads, kv, dim, first, second):
+    """One call for both kinds of requests takes no multiple of two calls' time."""
+    say(what)
+    one, two = (microseconds(call_of(*x, heads, kv, dim, 64)) for x in (first, second))
+    both = microseconds(call_of(first[0] + second[0], first[1] + second[1], heads, kv, dim, 64))
+    print("%s: %.1f and %.1f us alone, %.1f us together" % (what, one, two, both))
+    assert both < 1.7 * (one + two)
