@@ -605,6 +605,10 @@ typedef enum qw_dtype {
     QW_BF16 = 1 /* bfloat16 */
 } qw_dtype;
 
+/* May be added to `causal` of qw_kv_attention: rows of `out` that belong to no
+ * request become zero. */
+#define QW_KV_ZERO_REST 0x40000000
+
 /* Most requests of one qw_kv_plan call (their running sums are held in LDS). */
 #define QW_KV_PLAN_MAX_REQUESTS 8191
 
@@ -758,8 +762,12 @@ QW_API qw_status qw_kv_read(const int32_t *slots, int64_t tokens, const int8_t *
  *   max_context  at least the longest context (table_width * block_size at
  *                most is used); it sizes the grid
  *   scale        multiplies the scores (usually head_dim^-1/2)
+ *   causal       0: no causal mask; QW_KV_ZERO_REST (see out) may be added
  *   out          [tokens][q_heads][head_dim], contiguous (written); rows that
- *                belong to no request keep what they hold
+ *                belong to no request (those before cu_tokens[0] and from
+ *                cu_tokens[requests] on) keep what they hold, or become zero
+ *                with QW_KV_ZERO_REST; a request's behind its first max_new
+ *                keep it
  *   workspace    qw_kv_attention_workspace() bytes (may be null if that is 0)
  *
  * Errors: QW_ERROR_INVALID_VALUE (null pointer, negative size, a workspace
@@ -768,7 +776,8 @@ QW_API qw_status qw_kv_read(const int32_t *slots, int64_t tokens, const int8_t *
  * or each other, unknown dtype), QW_ERROR_UNSUPPORTED (head_dim, block_size,
  * stride not a multiple of 8, requests above 65535, max_new * q_heads above
  * 2^20, other sizes above 2^31 - 1), QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.
- * tokens == 0 or requests == 0 is a no-op.
+ * tokens == 0, requests == 0 or max_new == 0 is a no-op (whatever `causal`
+ * holds).
  *
  * qw_kv_attention_workspace -- workspace bytes for these sizes on the current
  * device (0: none needed), -1 for sizes that the call rejects.

@@ -321,7 +321,8 @@ QW_API qw_status qw_kv_attention(const void *q, int64_t q_stride, int dtype, int
                               (int32_t)q_heads, (int32_t)kv_heads, (int32_t)(q_heads / kv_heads), (int32_t)head_dim, k_cache, v_cache,
                               k_scales, v_scales, num_blocks, shift_of(block_size), block_table, (int32_t)table_width, context,
                               cu_tokens, (int32_t)requests, (int32_t)max_new, (int32_t)max_context,
-                              (float)(scale * 1.4426950408889634), causal != 0, (int32_t)window, static_cast<float *>(workspace)};
+                              (float)(scale * 1.4426950408889634), (causal & ~QW_KV_ZERO_REST) != 0, (int32_t)window, static_cast<float *>(workspace),
+                              (causal & QW_KV_ZERO_REST) != 0};
     return status_of(qw::launch_kv_attention(a, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -91,6 +91,18 @@ __device__ __forceinline__ Request request_of(const KvAttnArgs &a, int r)
     return s;
 }
 
+// The same, and behind the requests the tokens of none, whose rows see no key.
+__device__ __forceinline__ Request request_or_gap(const KvAttnArgs &a, int r)
+{
+    if (r < a.requests)
+        return request_of(a, r);
+    Request s;
+    static_cast<KvRequest &>(s) = kv_gap(a, r - a.requests);
+    s.lo = s.hi = 0;
+    s.cost = s.rows ? 1 + kUnitCost : 0;
+    return s;
+}
+
 // ---------------------------------------------------------------------------
 // Split kernel: the 64-key tiles of a unit (one key head and block of 16 RT
 // query rows of one request) are taken in turn by the waves of a workgroup,
@@ -164,7 +176,7 @@ struct Range {
             const int behind = before + s.template total<RT>(a);
             if (at >= behind) {
                 before = behind;
-                s = request_of(a, ++r);
+                s = request_or_gap(a, ++r);
                 continue;
             }
             const int rel = at - before;
@@ -445,6 +457,24 @@ __device__ __forceinline__ void split_piece(const KvAttnArgs &a, const Piece &p,
     __syncthreads();
 }
 
+// Zeroes the rows of no request, where that is asked for: by the first workgroups
+// of the unit form, when their own work is done (by all of them, when they begin:
+// 264 us for 248 for eight prompts of up to 4096 with 64 channels, 104 for 91 for
+// 1024 single tokens).
+__device__ __forceinline__ void zero_rest(const KvAttnArgs &a)
+{
+    const unsigned group = blockIdx.y * gridDim.x + blockIdx.x, all = gridDim.x * gridDim.y, groups = all < 256 ? all : 256;
+    if (!a.zero_rest || group >= groups)
+        return;
+    const int64_t row = (int64_t)a.q_heads * a.head_dim;
+    for (int g = 0; g < 2; ++g) {
+        const KvRequest s = kv_gap(a, g);
+        for (int64_t t = group; t < -s.past; t += groups)
+            for (int64_t i = threadIdx.x * 8; i < row; i += blockDim.x * 8)
+                *reinterpret_cast<u32x4_t *>(a.out + (s.t0 + t) * row + i) = (u32x4_t){0, 0, 0, 0};
+    }
+}
+
 // One workgroup a unit: for contexts that one workgroup reads fast enough,
 // or units enough to fill the chip many times over.
 template <int D, int RT, int DT, int LAYOUT, bool ONCE>
@@ -456,6 +486,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a)
     Piece p = {s, (int)blockIdx.y, (int)blockIdx.x - rb * a.kv_heads, rb * 16 * RT, s.lo, s.hi, nullptr};
     if (p.row0 < s.rows)
         split_piece<D, RT, DT, LAYOUT, ONCE>(a, p, lds);
+    zero_rest(a);
 }
 
 // The tiles of all units in a row, cut into equal ranges, split_groups a CU:
@@ -487,6 +518,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
     int32_t *head = reinterpret_cast<int32_t *>(a.workspace);
     Cut *cuts = reinterpret_cast<Cut *>(a.workspace);
 
+    const int requests = a.requests + (a.zero_rest ? 2 : 0); // with the gaps
+
     // Cost before each request of a batch of NT; `sum` grows by the batch's.
     auto scan = [&](int cost, int &sum) {
         int upto = cost;
@@ -507,14 +540,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
         return before;
     };
     auto batch = [&](int r) {
-        Request s = request_of(a, r < a.requests ? r : a.requests - 1);
-        s.cost = r < a.requests ? s.cost : 0;
+        Request s = request_or_gap(a, r < requests ? r : requests - 1);
+        s.cost = r < requests ? s.cost : 0;
         return s;
     };
 
     int total = 0, before = 0;
     Request mine;
-    for (int base = 0; base < a.requests; base += NT) {
+    for (int base = 0; base < requests; base += NT) {
         if (base)
             __syncthreads(); // wave_sums has been read
         const int r = base + (int)threadIdx.x;
@@ -539,9 +572,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_stream_kernel(KvAttnArgs a,
     range.parts = a.workspace + parts_offset(a.requests, gridDim.x) + (int64_t)blockIdx.x * 2 * piece_floats(D, RT);
     const int first = range.at;
     int sum = 0;
-    for (int base = 0; base < a.requests; base += NT) {
+    for (int base = 0; base < requests; base += NT) {
         const int r = base + (int)threadIdx.x;
-        if (a.requests > NT) { // once more, batch by batch
+        if (requests > NT) { // once more, batch by batch
             __syncthreads();
             mine = batch(r);
             before = scan(mine.template total<RT>(a), sum);
@@ -696,17 +729,19 @@ struct SplitShape {
 };
 
 // `rows`: the most query rows of a key head.
-SplitShape split_shape(int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t rows, int64_t max_new, int64_t max_context,
-                       int64_t window)
+SplitShape split_shape(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t rows, int64_t group,
+                       int64_t max_new, int64_t max_context, int64_t window)
 {
     SplitShape p;
     p.rt = rows <= 16 ? 1 : 2;
     p.units = (int)((rows + 16 * p.rt - 1) / (16 * p.rt) * kv_heads);
-    const int64_t tiles = longest_walk(max_new, max_context, window), all = (tiles + kUnitCost) * requests * p.units;
+    const int64_t tiles = longest_walk(max_new, max_context, window);
+    const int64_t gaps = 2 * (1 + kUnitCost) * (tokens * group / (16 * p.rt) + 1) * kv_heads; // tokens of no request
+    const int64_t all = (tiles + kUnitCost) * requests * p.units + gaps;
     // What the device's sums can reach (in int32) whatever the lengths it finds:
     // without a causal mask a window bounds no request's keys, if it has more
     // queries than max_new.
-    const int64_t most = ((max_context + kTile - 1) / kTile + kUnitCost) * requests * p.units;
+    const int64_t most = ((max_context + kTile - 1) / kTile + kUnitCost) * requests * p.units + gaps;
     p.groups = device_cu_count() * split_groups((int)head_dim, p.rt);
     // One workgroup a unit where a unit is short, or where units fill the chip
     // some times over (then the dispatch balances them, also the unequal row
@@ -739,7 +774,7 @@ AttnPlan attn_plan(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t h
 {
     AttnPlan p = {};
     p.prompt = prompt_preferred(tokens, requests, kv_heads, head_dim, group, max_new);
-    p.main = split_shape(requests, kv_heads, head_dim, max_new * group, max_new, max_context, window);
+    p.main = split_shape(tokens, requests, kv_heads, head_dim, max_new * group, group, max_new, max_context, window);
     // The prompt kernel, and the split kernel with a workgroup a unit, give all
     // the keys of a row block to one workgroup.  Where a request may have few rows
     // (some have fewer than max_new tokens) behind more keys than prompts have,
@@ -752,7 +787,7 @@ AttnPlan attn_plan(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t h
     const bool sparse = requests * p.main.units > 2 * (tokens * group / (16 * p.main.rt) + requests) * kv_heads;
     if (serial && max_new > few_new && tokens < requests * max_new &&
         longest_walk(max_new, max_context, window) >= (max_new + kTile - 1) / kTile + long_walk(p.prompt, sparse)) {
-        p.few = split_shape(requests, kv_heads, head_dim, few_new * group, few_new, max_context, window);
+        p.few = split_shape(tokens, requests, kv_heads, head_dim, few_new * group, group, few_new, max_context, window);
         p.rest = p.few.groups > 0;
         p.main_least = p.rest ? (int)(few_new * group) + 1 : 0;
     }
@@ -834,6 +869,7 @@ hipError_t launch_kv_attention(const KvAttnArgs &a, int dtype, hipStream_t strea
     const hipError_t e = p.prompt ? launch_kv_prompt(part, dtype, stream) : launch_split_any(part, p.main, dtype, stream);
     if (e != hipSuccess || !p.rest)
         return e;
+    part.zero_rest = false;
     part.least_rows = 0;
     part.most_rows = p.main_least - 1;
     return launch_split_any(part, p.few, dtype, stream);

@@ -42,6 +42,14 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs &a, int r)
     return s;
 }
 
+// The tokens of no request, as one without keys: those behind the last one's
+// (g = 0), and before the first one's (g = 1).
+__device__ __forceinline__ KvRequest kv_gap(const KvAttnArgs &a, int g)
+{
+    const int edge = kv_clamp(a.cu_tokens[g ? 0 : a.requests], 0, a.tokens), n = g ? edge : a.tokens - edge;
+    return {g ? 0 : edge, -n, 0, n * a.group};
+}
+
 // 8 activations -> fp16 (bf16 after multiplication by `up`, a power of two).
 template <int DT>
 __device__ __forceinline__ half8_t kv_half8(u32x4_t v, float up)

@@ -81,6 +81,7 @@ struct KvAttnArgs {
     float scale_log2; // softmax scale * log2(e)
     int32_t causal, window;
     float *workspace;
+    bool zero_rest = false;                         // rows of `out` that no request computes become zero
     int32_t least_rows = 0, most_rows = 0x7fffffff; // rows a key head of the requests that a launch takes
 };
 int device_cu_count(); // qw_api.hip

@@ -77,15 +77,18 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
     // the shader engines whatever they hold: with one long request among four,
     // 64 of 256 CUs worked), so the row blocks of all requests lie in a row, and
     // the host bounds their number by the tokens'.  Within a request the last
-    // rows come first: under a causal mask they have the most keys.
+    // rows come first: under a causal mask they have the most keys.  Tokens of no
+    // request come behind, if their rows are to be zeroed, as requests without keys.
     int target = (int)blockIdx.x / a.kv_heads;
     const int kvh = (int)blockIdx.x - target * a.kv_heads;
+    const int requests = a.requests + (a.zero_rest ? 2 : 0);
+    auto request = [&](int r) { return r < a.requests ? kv_request(a, r) : kv_gap(a, r - a.requests); };
     for (int base = 0;; base += kThreads) {
-        if (base >= a.requests)
+        if (base >= requests)
             return; // (the bound's slack)
         const int mine = base + tid;
-        const KvRequest q = kv_request(a, mine < a.requests ? mine : a.requests - 1);
-        const int blocks = mine < a.requests ? (q.rows + kRows - 1) / kRows : 0;
+        const KvRequest q = request(mine < requests ? mine : requests - 1);
+        const int blocks = mine < requests ? (q.rows + kRows - 1) / kRows : 0;
         int upto = blocks;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
     }
     const int r = __builtin_amdgcn_readfirstlane(lds.found[0]);
     const int row0 = __builtin_amdgcn_readfirstlane(lds.found[1]) * kRows;
-    const KvRequest s = kv_request(a, r);
+    const KvRequest s = request(r);
     __syncthreads(); // lds is the tiles' from here on
     const int last_row = row0 + kRows < s.rows ? row0 + kRows - 1 : s.rows - 1;
     const int first_i = row0 / a.group, last_i = last_row / a.group;
@@ -421,7 +424,7 @@ hipError_t launch_kv_prompt(const KvAttnArgs &a, int dtype, hipStream_t stream)
     // row blocks of all requests: full ones of the tokens' rows, and a last one each
     const int64_t each = ((int64_t)a.max_new * a.group + kRows - 1) / kRows * a.requests;
     const int64_t full = (int64_t)a.tokens * a.group / kRows + a.requests;
-    const dim3 grid((unsigned)((each < full ? each : full) * a.kv_heads));
+    const dim3 grid((unsigned)((a.zero_rest ? full + 2 : each < full ? each : full) * a.kv_heads));
     if (dtype == QW_F16)
         kv_prompt_kernel<QW_F16><<<grid, dim3(kThreads), 0, stream>>>(a);
     else

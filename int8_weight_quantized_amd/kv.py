@@ -23,6 +23,7 @@ import int8_weight_quantized_amd as _pkg  # (partly initialised here; its attrib
 KV_HEAD_DIMS = (64, 128)
 KV_BLOCK_SIZES = (16, 32, 64, 128)
 KV_PLAN_MAX_REQUESTS = 8191
+KV_ZERO_REST = 0x40000000
 
 
 class KvCache(NamedTuple):
@@ -440,7 +441,8 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
     request, max_context at least the longest context (default: what the
     table holds); both are host numbers that size the launch.  window > 0
     lets a query see that many keys, its own the last.  Rows that see
-    nothing are zero.  ``workspace`` (uint8, kv_attention_workspace bytes) is
+    nothing are zero.  Rows of no request (padding behind the last one's tokens)
+    are zero too, or keep what a given ``out`` holds there.  ``workspace`` (uint8, kv_attention_workspace bytes) is
     allocated when not given.  Returns [T, Hq, D]."""
     torch = _torch or _load_torch()
     try:
@@ -465,6 +467,9 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
         fine = fine and max_context >= 0
     except (AttributeError, KeyError, TypeError, ValueError, IndexError, ZeroDivisionError):
         fine = False
+    mask = 1 if causal else 0
+    if out is None:
+        mask |= KV_ZERO_REST  # an output allocated here holds nothing to keep
     if fine:
         if scale is None:
             scale = 1.0 / math.sqrt(dim)
@@ -475,6 +480,8 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
             q, (k_cache, v_cache, k_scales, v_scales), block_table, context, cu_tokens, max_new, max_context, scale, window, out,
             device)
         index = q.get_device()
+    if mask & KV_ZERO_REST and (requests == 0 or max_new == 0):
+        return out.zero_()
     lib = _pkg.library()
     if workspace is None:
         need = lib.qw_kv_attention_workspace(tokens, heads, kv_heads, dim, size, width, requests, max_new, max_context, window)
@@ -486,7 +493,7 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
     status = lib.qw_kv_attention(
         q.data_ptr(), sq, code, tokens, heads, kv_heads, dim, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
         v_scales.data_ptr(), blocks, size, block_table.data_ptr(), width, context.data_ptr(), cu_tokens.data_ptr(), requests,
-        max_new, max_context, scale, 1 if causal else 0, window, out.data_ptr(),
+        max_new, max_context, scale, mask, window, out.data_ptr(),
         None if workspace is None else workspace.data_ptr(), need if need > 0 else 0, _raw_stream(index))
     if status:
         _raise(status, "qw_kv_attention")
