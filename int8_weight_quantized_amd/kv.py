@@ -71,11 +71,10 @@ _raw_stream = None
 def _load_torch():
     global _torch, _raw_stream
     import torch
-    _torch = torch
     _codes.update({torch.float16: 0, torch.bfloat16: 1})
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if _raw_stream is None:
-        _raw_stream = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch  # last: another thread that sees it uses the others
     return torch
 
 
