@@ -311,6 +311,16 @@ def _stream_of(t) -> int:
     return int(torch.cuda.current_stream(t.device).cuda_stream)
 
 
+def _on_device(index, call, *args):
+    """call(*args) with GPU `index` current: a kernel is launched on the
+    current device, whatever device its stream and its operands are of."""
+    torch = _torch()
+    if index is None or index < 0 or torch.cuda.current_device() == index:
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
+
+
 def _check(t, name, dtype, shape=None, ndim=None, device=None):
     """Validate one tensor argument before its pointer reaches the library:
     a torch.Tensor of `dtype`, contiguous, with exactly `shape` (or `ndim`
@@ -409,7 +419,7 @@ def quantize_weights(w, clip_percentile: float = 100.0, out=None):
     device = _require_gpu(w, "w")
     f16, n, k, q, s = _validate_quantize(w, out, device)
     raw = quantize_weights_f16_raw if f16 else quantize_weights_raw
-    st = raw(w.data_ptr(), n, k, clip_percentile, q.data_ptr(), s.data_ptr(), _stream_of(w))
+    st = _on_device(device.index, raw, w.data_ptr(), n, k, clip_percentile, q.data_ptr(), s.data_ptr(), _stream_of(w))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_quantize_weights_f16" if f16 else "qw_quantize_weights")
     return q, s
@@ -420,8 +430,8 @@ def w8a16_gemm(x, q, scales, out=None, path: str = "auto"):
     -> fp16 [M, N].  ``path`` forces a kernel ("gemv", "skinny" or "mfma")."""
     device = _require_gpu(x, "x")
     m, n, k, _, y = _validate_gemm(x, q, scales, out, path, device)
-    st = w8a16_gemm_raw(x.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(), m, n, k,
-                        _stream_of(x), PATHS[path])
+    st = _on_device(device.index, w8a16_gemm_raw, x.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(), m, n, k,
+                    _stream_of(x), PATHS[path])
     if st != QW_SUCCESS:
         raise QwError(st, "qw_w8a16_gemm")
     return y
@@ -433,7 +443,8 @@ def w8a16_gemm_tune(x, q, scales, out=None):
     result).  Later automatic calls of the bucket use the record."""
     device = _require_gpu(x, "x")
     m, n, k, _, y = _validate_gemm(x, q, scales, out, None, device)
-    st = w8a16_gemm_tune_raw(x.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(), m, n, k, _stream_of(x))
+    st = _on_device(device.index, w8a16_gemm_tune_raw, x.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(), m,
+                    n, k, _stream_of(x))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_w8a16_gemm_tune")
     return y
@@ -454,8 +465,8 @@ def quantize_weights_fixed_range(w, bounds, out=None):
     (q int8 [N, K], scales float16 [N])."""
     device = _require_gpu(w, "w")
     n, k, q, s = _validate_fixed_range(w, bounds, out, device)
-    st = quantize_weights_fixed_range_raw(w.data_ptr(), n, k, bounds.data_ptr(), q.data_ptr(), s.data_ptr(),
-                                          _stream_of(w))
+    st = _on_device(device.index, quantize_weights_fixed_range_raw, w.data_ptr(), n, k, bounds.data_ptr(), q.data_ptr(),
+                    s.data_ptr(), _stream_of(w))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_quantize_weights_fixed_range")
     return q, s
@@ -475,8 +486,8 @@ def quantize_weights_outliers(w, clip_percentile: float):
     # (at least one slot allocated, so that the pointers are valid with cap 0)
     idx = torch.empty((n, max(cap, 1)), dtype=torch.int32, device=device)[:, :cap]
     val = torch.empty((n, max(cap, 1)), dtype=torch.float32, device=device)[:, :cap]
-    st = quantize_weights_outliers_raw(w.data_ptr(), n, k, clip_percentile, q.data_ptr(), s.data_ptr(),
-                                       idx.data_ptr(), val.data_ptr(), cap, _stream_of(w))
+    st = _on_device(device.index, quantize_weights_outliers_raw, w.data_ptr(), n, k, clip_percentile, q.data_ptr(),
+                    s.data_ptr(), idx.data_ptr(), val.data_ptr(), cap, _stream_of(w))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_quantize_weights_outliers")
     return q, s, idx, val
@@ -488,8 +499,8 @@ def w8a16_gemm_outliers(x, q, scales, ol_idx, ol_val, out=None, path: str = "aut
     float32 [N, C] -> fp16 [M, N]."""
     device = _require_gpu(x, "x")
     m, n, k, cap, y = _validate_gemm(x, q, scales, out, path, device, ol=(ol_idx, ol_val))
-    st = w8a16_gemm_outliers_raw(x.data_ptr(), q.data_ptr(), scales.data_ptr(), ol_idx.data_ptr(),
-                                 ol_val.data_ptr(), cap, y.data_ptr(), m, n, k, _stream_of(x), PATHS[path])
+    st = _on_device(device.index, w8a16_gemm_outliers_raw, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                    ol_idx.data_ptr(), ol_val.data_ptr(), cap, y.data_ptr(), m, n, k, _stream_of(x), PATHS[path])
     if st != QW_SUCCESS:
         raise QwError(st, "qw_w8a16_gemm_outliers")
     return y
@@ -507,9 +518,9 @@ def w8a16_gemm_tile(x, q, scales, tile, zeros=None, outliers=None, out=None):
     m, n, k, cap, y = _validate_gemm(x, q, scales, out, None, device, zeros=zeros, ol=outliers)
     idx_ptr = outliers[0].data_ptr() if outliers is not None else None
     val_ptr = outliers[1].data_ptr() if outliers is not None else None
-    st = w8a16_gemm_tile_raw(x.data_ptr(), q.data_ptr(), scales.data_ptr(),
-                             zeros.data_ptr() if zeros is not None else None, idx_ptr, val_ptr, cap,
-                             y.data_ptr(), m, n, k, tile[0] * 1000 + tile[1], _stream_of(x))
+    st = _on_device(device.index, w8a16_gemm_tile_raw, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                    zeros.data_ptr() if zeros is not None else None, idx_ptr, val_ptr, cap, y.data_ptr(), m, n, k,
+                    tile[0] * 1000 + tile[1], _stream_of(x))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_w8a16_gemm_tile")
     return y
@@ -525,7 +536,8 @@ def quantize_weights_asym(w, out=None):
     n, k = w.shape
     q, s, z = _outputs(out, (("q", torch.int8, (n, k)), ("scales", torch.float16, (n,)),
                              ("zeros", torch.int8, (n,))), device)
-    st = quantize_weights_asym_raw(w.data_ptr(), n, k, q.data_ptr(), s.data_ptr(), z.data_ptr(), _stream_of(w))
+    st = _on_device(device.index, quantize_weights_asym_raw, w.data_ptr(), n, k, q.data_ptr(), s.data_ptr(),
+                    z.data_ptr(), _stream_of(w))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_quantize_weights_asym")
     return q, s, z
@@ -536,8 +548,8 @@ def w8a16_gemm_asym(x, q, scales, zeros, out=None, path: str = "auto"):
     [M, K], q int8 [N, K], scales fp16 [N], zeros int8 [N] -> fp16 [M, N]."""
     device = _require_gpu(x, "x")
     m, n, k, _, y = _validate_gemm(x, q, scales, out, path, device, zeros=zeros)
-    st = w8a16_gemm_asym_raw(x.data_ptr(), q.data_ptr(), scales.data_ptr(), zeros.data_ptr(), y.data_ptr(),
-                             m, n, k, _stream_of(x), PATHS[path])
+    st = _on_device(device.index, w8a16_gemm_asym_raw, x.data_ptr(), q.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+                    y.data_ptr(), m, n, k, _stream_of(x), PATHS[path])
     if st != QW_SUCCESS:
         raise QwError(st, "qw_w8a16_gemm_asym")
     return y
@@ -555,8 +567,8 @@ def w8a8_gemm(qx, sx, q, scales, out=None):
     [M], q int8 [N, K], scales fp16 [N] -> fp16 [M, N]."""
     device = _require_gpu(qx, "qx")
     m, n, k, _, y = _validate_gemm(qx, q, scales, out, None, device, a8=True, sx=sx)
-    st = w8a8_gemm_raw(qx.data_ptr(), sx.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(),
-                       m, n, k, _stream_of(qx))
+    st = _on_device(device.index, w8a8_gemm_raw, qx.data_ptr(), sx.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                    y.data_ptr(), m, n, k, _stream_of(qx))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_w8a8_gemm")
     return y
@@ -569,8 +581,8 @@ def w8a8_gemm_tile(qx, sx, q, scales, tile, out=None):
         raise ValueError("tile must be one of %s, got %r" % (W8A8_TILES, tile))
     device = _require_gpu(qx, "qx")
     m, n, k, _, y = _validate_gemm(qx, q, scales, out, None, device, a8=True, sx=sx)
-    st = w8a8_gemm_tile_raw(qx.data_ptr(), sx.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(),
-                            m, n, k, tile[0] * 1000 + tile[1], _stream_of(qx))
+    st = _on_device(device.index, w8a8_gemm_tile_raw, qx.data_ptr(), sx.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                    y.data_ptr(), m, n, k, tile[0] * 1000 + tile[1], _stream_of(qx))
     if st != QW_SUCCESS:
         raise QwError(st, "qw_w8a8_gemm_tile")
     return y

@@ -62,18 +62,22 @@ def _declare(lib):
 # The calls below are a few microseconds of kernel each in decode, so their
 # own time counts.  Each first tests its arguments with plain attribute
 # reads; only where that fails do the _validate_* helpers run, which say what
-# is wrong (and let pass what the quick test was too narrow for).
+# is wrong (and let pass what the quick test was too narrow for).  A kernel is
+# launched on the current device, so a call whose operands are on another one
+# begins again with that one current.
 
 _torch = None
 _raw_stream = None
+_current_device = None
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     import torch
     _codes.update({torch.float16: 0, torch.bfloat16: 1})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch  # last: another thread that sees it uses the others
     return torch
 
@@ -203,6 +207,8 @@ def kv_plan(past, fresh, block_table, free_blocks, block_size: int, max_tokens: 
         device = _pkg._require_gpu(past, "past")
         requests = _validate_plan(past, fresh, block_table, free_blocks, block_size, max_tokens, device)
         index, width, n_free = past.get_device(), block_table.shape[1], free_blocks.shape[0]
+    if index != _current_device():
+        return _pkg._on_device(index, kv_plan, past, fresh, block_table, free_blocks, block_size, max_tokens)
     # one allocation for the five arrays
     buf = torch.empty(2 * requests + 3 + 2 * max_tokens, dtype=i32, device=past.device)
     cu, context, counts, positions, slots = buf.split_with_sizes((requests + 1, requests, 2, max_tokens, max_tokens))
@@ -210,9 +216,9 @@ def kv_plan(past, fresh, block_table, free_blocks, block_size: int, max_tokens: 
     p_ctx = p + 4 * (requests + 1)
     p_counts = p_ctx + 4 * requests
     p_pos = p_counts + 8
-    status = _pkg.library().qw_kv_plan(past.data_ptr(), fresh.data_ptr(), requests, block_table.data_ptr(), width,
-                                       free_blocks.data_ptr(), n_free, block_size, max_tokens, p, p_ctx, p_pos,
-                                       p_pos + 4 * max_tokens, p_counts, _raw_stream(index))
+    status = _pkg.library().qw_kv_plan(
+        past.data_ptr(), fresh.data_ptr(), requests, block_table.data_ptr(), width, free_blocks.data_ptr(), n_free, block_size,
+        max_tokens, p, p_ctx, p_pos, p_pos + 4 * max_tokens, p_counts, _raw_stream(index))
     if status:
         _raise(status, "qw_kv_plan")
     return KvPlan(block_table, cu, context, positions, slots, counts)
@@ -288,6 +294,8 @@ def qk_norm_rope(q, k, positions, cos, sin, q_weight=None, k_weight=None, eps: f
         code, tokens, hq, hk, dim, rot, sq, sk, qo, sqo, ko, sko = _validate_norm_rope(
             q, k, positions, cos, sin, q_weight, k_weight, out, device)
         index, span = q.get_device(), cos.shape[0]
+    if index != _current_device():
+        return _pkg._on_device(index, qk_norm_rope, q, k, positions, cos, sin, q_weight, k_weight, eps, interleaved, out)
     status = _pkg.library().qw_qk_norm_rope(
         q.data_ptr(), sq, k.data_ptr(), sk, code, tokens, hq, hk, dim, positions.data_ptr(), cos.data_ptr(), sin.data_ptr(),
         span, rot, 1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
@@ -347,6 +355,8 @@ def kv_write(k, v, slots, k_cache, v_cache, k_scales, v_scales) -> None:
         device = _pkg._require_gpu(k, "k")
         code, tokens, heads, dim, sk, sv, blocks, size = _validate_write(k, v, slots, (k_cache, v_cache, k_scales, v_scales), device)
         index = k.get_device()
+    if index != _current_device():
+        return _pkg._on_device(index, kv_write, k, v, slots, k_cache, v_cache, k_scales, v_scales)
     status = _pkg.library().qw_kv_write(
         k.data_ptr(), sk, v.data_ptr(), sv, code, tokens, heads, dim, slots.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), blocks, size, _raw_stream(index))
@@ -380,6 +390,8 @@ def kv_read(slots, k_cache, v_cache, k_scales, v_scales, dtype=None):
         device = _pkg._require_gpu(slots, "slots")
         code, tokens, blocks, heads, size, dim = _validate_read(slots, (k_cache, v_cache, k_scales, v_scales), dtype, device)
         index = slots.get_device()
+    if index != _current_device():
+        return _pkg._on_device(index, kv_read, slots, k_cache, v_cache, k_scales, v_scales, dtype)
     k = torch.empty((tokens, heads, dim), dtype=dtype, device=slots.device)
     v = torch.empty_like(k)
     status = _pkg.library().qw_kv_read(
@@ -423,9 +435,9 @@ def kv_attention_workspace(q, k_cache, block_table, max_new: int, max_context=No
     tokens, heads, dim = q.shape
     requests, width = block_table.shape
     size = k_cache.shape[2]
-    n = int(_pkg.library().qw_kv_attention_workspace(
-        tokens, heads, k_cache.shape[1], dim, size, width, requests, max_new,
-        width * size if max_context is None else max_context, window))
+    n = int(_pkg._on_device(
+        q.get_device(), _pkg.library().qw_kv_attention_workspace, tokens, heads, k_cache.shape[1], dim, size, width, requests,
+        max_new, width * size if max_context is None else max_context, window))
     if n < 0:
         raise ValueError("kv_attention does not take these sizes")
     return n
@@ -466,7 +478,7 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
         fine = fine and max_context >= 0
     except (AttributeError, KeyError, TypeError, ValueError, IndexError, ZeroDivisionError):
         fine = False
-    mask = 1 if causal else 0
+    mask, given = 1 if causal else 0, out
     if out is None:
         mask |= KV_ZERO_REST  # an output allocated here holds nothing to keep
     if fine:
@@ -479,6 +491,9 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, context, 
             q, (k_cache, v_cache, k_scales, v_scales), block_table, context, cu_tokens, max_new, max_context, scale, window, out,
             device)
         index = q.get_device()
+    if index != _current_device():
+        return _pkg._on_device(index, kv_attention, q, k_cache, v_cache, k_scales, v_scales, block_table, context, cu_tokens,
+                               max_new, max_context, scale, causal, window, given, workspace)
     if mask & KV_ZERO_REST and (requests == 0 or max_new == 0):
         return out.zero_()
     lib = _pkg.library()
