@@ -774,8 +774,9 @@ QW_API qw_status qw_kv_read(const int32_t *slots, int64_t tokens, const int8_t *
  * that is too small, scale not finite, q_heads not a multiple of kv_heads,
  * a stride below q_heads * head_dim, out or workspace overlapping an input
  * or each other, unknown dtype), QW_ERROR_UNSUPPORTED (head_dim, block_size,
- * stride not a multiple of 8, requests above 65535, max_new * q_heads above
- * 2^20, other sizes above 2^31 - 1), QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.
+ * stride not a multiple of 8, requests above 65535, max_new above 2^20,
+ * min(max_new, tokens) * q_heads above 2^23, other sizes above 2^31 - 1),
+ * QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.
  * tokens == 0, requests == 0 or max_new == 0 is a no-op (whatever `causal`
  * holds).
  *

@@ -106,7 +106,10 @@ qw_status check_cache(const CacheShape &c)
     return QW_SUCCESS;
 }
 
-// Sizes of an attention call; kv_heads divides q_heads.
+int64_t smaller(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// Sizes of an attention call; kv_heads divides q_heads.  A request has as many
+// queries as the call at most; 2^23 of its rows are 2^31 threads of the join.
 qw_status check_attention_sizes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t block_size,
                                 int64_t table_width, int64_t requests, int64_t max_new, int64_t max_context, int64_t window)
 {
@@ -114,13 +117,11 @@ qw_status check_attention_sizes(int64_t tokens, int64_t q_heads, int64_t kv_head
         table_width < 0 || q_heads % kv_heads)
         return QW_ERROR_INVALID_VALUE;
     if (!head_dim_ok(head_dim) || shift_of(block_size) < 0 || tokens > kMaxDim || requests > 65535 || q_heads > 65535 ||
-        max_new > (1 << 20) || max_new * q_heads > (1 << 20) || table_width > kMaxDim || max_context > kMaxDim - 4096 ||
-        window > kMaxDim)
+        max_new > (1 << 20) || smaller(max_new, tokens) * q_heads > (1 << 23) || table_width > kMaxDim ||
+        max_context > kMaxDim - 4096 || window > kMaxDim)
         return QW_ERROR_UNSUPPORTED;
     return QW_SUCCESS;
 }
-
-int64_t smaller(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // What the sizes mean to the kernels: a context the table can hold, and no
 // window where it hides nothing.
