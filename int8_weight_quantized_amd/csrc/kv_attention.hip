@@ -476,16 +476,27 @@ __device__ __forceinline__ void zero_rest(const KvAttnArgs &a)
 }
 
 // One workgroup a unit: for contexts that one workgroup reads fast enough,
-// or units enough to fill the chip many times over.
+// or units enough to fill the chip many times over.  The grid is units and
+// requests, or (`dense`) the row blocks that there are at most: where the
+// requests' numbers of rows differ much most workgroups of the first find none,
+// at 1 ns each (one prompt of 4096 beside 255 tokens, 16 heads of 64, behind
+// 500: 529 us and 125; 1024 single tokens, all of them there, 91 and 95).
 template <int D, int RT, int DT, int LAYOUT, bool ONCE>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a)
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_unit_kernel(KvAttnArgs a, bool dense)
 {
     __shared__ __attribute__((aligned(16))) SplitLds<D, RT> lds;
-    const Request s = request_of(a, blockIdx.y);
-    const int rb = (int)blockIdx.x / a.kv_heads;
-    Piece p = {s, (int)blockIdx.y, (int)blockIdx.x - rb * a.kv_heads, rb * 16 * RT, s.lo, s.hi, nullptr};
-    if (p.row0 < s.rows)
-        split_piece<D, RT, DT, LAYOUT, ONCE>(a, p, lds);
+    __shared__ int sums[kWaves], found[2];
+    int rb = (int)blockIdx.x / a.kv_heads, r = blockIdx.y;
+    const int kvh = (int)blockIdx.x - rb * a.kv_heads;
+    bool any = true;
+    if (dense)
+        any = kv_find_block<kWaves>(a.requests, 16 * RT, [&](int i) { return kv_request(a, i).rows; }, rb, sums, found, r, rb);
+    if (any) {
+        const Request s = request_of(a, r);
+        const Piece p = {s, r, kvh, rb * 16 * RT, s.lo, s.hi, nullptr};
+        if (p.row0 < s.rows)
+            split_piece<D, RT, DT, LAYOUT, ONCE>(a, p, lds);
+    }
     zero_rest(a);
 }
 
@@ -725,7 +736,9 @@ bool prompt_preferred(int64_t tokens, int64_t requests, int64_t kv_heads, int64_
 
 struct SplitShape {
     int rt, units;
-    int groups; // workgroups of the streamed form; 0: one a unit
+    int64_t live; // units of all requests, by the number of tokens
+    bool sparse;  // a fraction of requests times units
+    int groups;   // workgroups of the streamed form; 0: one a unit
 };
 
 // `rows`: the most query rows of a key head.
@@ -735,6 +748,8 @@ SplitShape split_shape(int64_t tokens, int64_t requests, int64_t kv_heads, int64
     SplitShape p;
     p.rt = rows <= 16 ? 1 : 2;
     p.units = (int)((rows + 16 * p.rt - 1) / (16 * p.rt) * kv_heads);
+    p.live = (tokens * group / (16 * p.rt) + requests) * kv_heads;
+    p.sparse = requests * p.units > 2 * p.live;
     const int64_t tiles = longest_walk(max_new, max_context, window);
     const int64_t gaps = 2 * (1 + kUnitCost) * (tokens * group / (16 * p.rt) + 1) * kv_heads; // tokens of no request
     const int64_t all = (tiles + kUnitCost) * requests * p.units + gaps;
@@ -784,9 +799,8 @@ AttnPlan attn_plan(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t h
     // chunks of up to 512 behind 15000, which gain nothing, 570 / 570.
     const int64_t few_new = group < 32 ? 32 / group : 1;
     const bool serial = p.prompt || p.main.groups == 0;
-    const bool sparse = requests * p.main.units > 2 * (tokens * group / (16 * p.main.rt) + requests) * kv_heads;
     if (serial && max_new > few_new && tokens < requests * max_new &&
-        longest_walk(max_new, max_context, window) >= (max_new + kTile - 1) / kTile + long_walk(p.prompt, sparse)) {
+        longest_walk(max_new, max_context, window) >= (max_new + kTile - 1) / kTile + long_walk(p.prompt, p.main.sparse)) {
         p.few = split_shape(tokens, requests, kv_heads, head_dim, few_new * group, group, few_new, max_context, window);
         p.rest = p.few.groups > 0;
         p.main_least = p.rest ? (int)(few_new * group) + 1 : 0;
@@ -798,7 +812,8 @@ template <int D, int RT, int DT, int LAYOUT, bool ONCE>
 hipError_t launch_split(const KvAttnArgs &a, const SplitShape &p, hipStream_t stream)
 {
     if (p.groups == 0) {
-        kv_unit_kernel<D, RT, DT, LAYOUT, ONCE><<<dim3((unsigned)p.units, (unsigned)a.requests), dim3(64 * kWaves), 0, stream>>>(a);
+        const dim3 grid = p.sparse ? dim3((unsigned)p.live) : dim3((unsigned)p.units, (unsigned)a.requests);
+        kv_unit_kernel<D, RT, DT, LAYOUT, ONCE><<<grid, dim3(64 * kWaves), 0, stream>>>(a, p.sparse);
         return hipGetLastError();
     }
     const int bound = a.max_new * a.group, rows = bound < a.most_rows ? bound : a.most_rows; // of a key head

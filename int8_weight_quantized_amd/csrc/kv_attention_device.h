@@ -50,6 +50,50 @@ __device__ __forceinline__ KvRequest kv_gap(const KvAttnArgs &a, int g)
     return {g ? 0 : edge, -n, 0, n * a.group};
 }
 
+// Row block number `target` of all requests' in a row, `per` rows a block: its
+// request and its number in it, or false behind the last one.  Within a request
+// the last rows come first: under a causal mask they have the most keys.  For
+// workgroups of 64 NW threads; `sums` and `found` are theirs, free to use.
+template <int NW, typename Rows>
+__device__ __forceinline__ bool kv_find_block(int requests, int per, Rows rows_of, int target, int *sums, int *found, int &request,
+                                              int &block)
+{
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    for (int base = 0;; base += 64 * NW) {
+        if (base >= requests)
+            return false;
+        const int mine = base + (int)threadIdx.x;
+        const int rows = rows_of(mine < requests ? mine : requests - 1);
+        const int blocks = mine < requests ? (rows + per - 1) / per : 0;
+        int upto = blocks;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(upto, d);
+            upto += lane >= d ? up : 0;
+        }
+        if (lane == 63)
+            sums[wave] = upto;
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            upto += w < wave ? sums[w] : 0;
+            total += sums[w];
+        }
+        if (target < upto && target >= upto - blocks) {
+            found[0] = mine;
+            found[1] = upto - 1 - target;
+        }
+        __syncthreads();
+        if (target < total)
+            break;
+        target -= total;
+    }
+    request = __builtin_amdgcn_readfirstlane(found[0]);
+    block = __builtin_amdgcn_readfirstlane(found[1]);
+    return true;
+}
+
 // 8 activations -> fp16 (bf16 after multiplication by `up`, a power of two).
 template <int DT>
 __device__ __forceinline__ half8_t kv_half8(u32x4_t v, float up)

@@ -76,45 +76,16 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prompt_kernel(KvAttnArgs a)
     // hold up the dispatch (each waits for a CU's LDS, and workgroups go round
     // the shader engines whatever they hold: with one long request among four,
     // 64 of 256 CUs worked), so the row blocks of all requests lie in a row, and
-    // the host bounds their number by the tokens'.  Within a request the last
-    // rows come first: under a causal mask they have the most keys.  Tokens of no
-    // request come behind, if their rows are to be zeroed, as requests without keys.
-    int target = (int)blockIdx.x / a.kv_heads;
+    // the host bounds their number by the tokens'.  Tokens of no request come behind,
+    // if their rows are to be zeroed, as requests without keys.
+    const int target = (int)blockIdx.x / a.kv_heads;
     const int kvh = (int)blockIdx.x - target * a.kv_heads;
-    const int requests = a.requests + (a.zero_rest ? 2 : 0);
     auto request = [&](int r) { return r < a.requests ? kv_request(a, r) : kv_gap(a, r - a.requests); };
-    for (int base = 0;; base += kThreads) {
-        if (base >= requests)
-            return; // (the bound's slack)
-        const int mine = base + tid;
-        const KvRequest q = request(mine < requests ? mine : requests - 1);
-        const int blocks = mine < requests ? (q.rows + kRows - 1) / kRows : 0;
-        int upto = blocks;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(upto, d);
-            upto += lane >= d ? up : 0;
-        }
-        if (lane == 63)
-            lds.sums[wave] = upto;
-        __syncthreads();
-        int total = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            upto += w < wave ? lds.sums[w] : 0;
-            total += lds.sums[w];
-        }
-        if (target < upto && target >= upto - blocks) {
-            lds.found[0] = mine;
-            lds.found[1] = upto - 1 - target;
-        }
-        __syncthreads();
-        if (target < total)
-            break;
-        target -= total;
-    }
-    const int r = __builtin_amdgcn_readfirstlane(lds.found[0]);
-    const int row0 = __builtin_amdgcn_readfirstlane(lds.found[1]) * kRows;
+    int r, row_block;
+    if (!kv_find_block<kWaves>(a.requests + (a.zero_rest ? 2 : 0), kRows, [&](int i) { return request(i).rows; }, target, lds.sums,
+                               lds.found, r, row_block))
+        return; // (the bound's slack)
+    const int row0 = row_block * kRows;
     const KvRequest s = request(r);
     __syncthreads(); // lds is the tiles' from here on
     const int last_row = row0 + kRows < s.rows ? row0 + kRows - 1 : s.rows - 1;

@@ -99,6 +99,19 @@ def test_groups_of_heads_beside_long_contexts(heads, kv, dim, tokens):
     compare(rng, new, [n + p for n, p in zip(new, past)], heads, kv, 16, BF16, dim=dim, prompt=False)
 
 
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 70)])
+@pytest.mark.parametrize("requests,heads,kv,dim,most", [(41, 16, 16, 64, 200), (300, 16, 16, 64, 130), (256, 12, 2, 64, 400),
+                                                        (60, 32, 2, 128, 33)])
+def test_few_of_the_row_blocks_are_there(requests, heads, kv, dim, most, causal, window):
+    """Requests with one or no new token, and two with many: the row blocks of
+    all of them in a row, more requests than a workgroup has threads among them."""
+    rng = np.random.default_rng(requests)
+    new = [int(n) for n in rng.integers(0, 2, requests)]
+    new[1], new[requests - 1] = most - 1, most
+    context = [n + int(p) for n, p in zip(new, rng.integers(0, 90, requests))]
+    compare(rng, new, context, heads, kv, 64, F16, causal=causal, window=window, dim=dim, prompt=False)
+
+
 @pytest.mark.parametrize("requests,heads,kv,dim", [(200, 16, 16, 64), (1100, 4, 2, 128)])
 def test_many_tokens_and_one_long_context(requests, heads, kv, dim):
     rng = np.random.default_rng(requests)
@@ -111,6 +124,7 @@ def test_many_tokens_and_one_long_context(requests, heads, kv, dim):
     ("a prompt beside one token", 32, 2, 128, ([4096], [4096]), ([1], [131072])),
     ("a prompt beside 63 tokens", 32, 2, 128, ([512], [512]), ([1] * 63, [8000] * 63)),
     ("a prompt beside one token, 64 channels", 16, 16, 64, ([4096], [4096]), ([1], [131072])),
+    ("a prompt beside 255 tokens, 64 channels", 16, 16, 64, ([4096], [4096]), ([1] * 255, [500] * 255)),
     ("192 tokens, one far behind", 16, 16, 64, ([1] * 191, [1000] * 191), ([1], [131072])),
 ])
 def test_a_long_context_is_shared_out(what, heads, kv, dim, first, second):

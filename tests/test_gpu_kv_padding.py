@@ -21,6 +21,7 @@ CASES = {
     "many rows, requests without tokens": (64, 8, 128, 1000, [0, 0, 450], [3, 450], 450),
     "ranges, a batch of requests": (4, 2, 64, 261, list(range(2, 259)), [3000, 20] * 128, 1),
     "ranges, more than a batch": (4, 2, 64, 270, list(range(2, 260)), [20, 3000, 0] * 85 + [7, 9], 1),
+    "few of the row blocks": (16, 16, 64, 300, [5] + list(range(205, 246)), [300] + [30] * 40, 200),
     "no request has tokens": (4, 2, 64, 7, [0, 0, 0], [40, 60], 3),
 }
 
