@@ -48,7 +48,7 @@ constexpr int kWaves = 4; // of a split workgroup
 // 70 us of the prompt kernel, at 2.3 a tile, or of the split kernel, at 0.5.
 // There a quarter of that where most workgroups find no rows: they pass through
 // what slots the long ones leave (64 requests, one of 512 tokens and the others
-// of one behind 8000: 451 us and 86).  (32 always: eight windowed chunks of 64
+// of one behind 8000: 451 us and 62).  (32 always: eight windowed chunks of 64
 // channels, up to 72 tiles and half of the workgroups empty, 96 us for 91.)
 constexpr int long_walk(bool prompt, bool sparse) { return prompt || sparse ? 32 : 128; }
 
@@ -741,9 +741,10 @@ struct SplitShape {
     int groups;   // workgroups of the streamed form; 0: one a unit
 };
 
-// `rows`: the most query rows of a key head.
+// `rows`: the most query rows of a key head.  `ranges`: whether to take ranges
+// however many units there are.
 SplitShape split_shape(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t head_dim, int64_t rows, int64_t group,
-                       int64_t max_new, int64_t max_context, int64_t window)
+                       int64_t max_new, int64_t max_context, int64_t window, bool ranges)
 {
     SplitShape p;
     p.rt = rows <= 16 ? 1 : 2;
@@ -767,7 +768,7 @@ SplitShape split_shape(int64_t tokens, int64_t requests, int64_t kv_heads, int64
     // workgroup's work (192 tokens behind 1000, 16 heads of 64: 58 us so, 67 in
     // ranges, but 686 and 113 if one of them stands behind 131072; all behind 4000
     // 237 and 244, behind 8000 473 and 481).
-    const bool fill = requests * p.units >= 4 * (int64_t)p.groups && (p.units > kv_heads || tiles <= 64);
+    const bool fill = !ranges && requests * p.units >= 4 * (int64_t)p.groups && (p.units > kv_heads || tiles <= 64);
     if (tiles <= 8 || most >= (int64_t(1) << 31) - (1 << 20) || fill)
         p.groups = 0;
     else if (all < kMinRange * (int64_t)p.groups)
@@ -789,19 +790,20 @@ AttnPlan attn_plan(int64_t tokens, int64_t requests, int64_t kv_heads, int64_t h
 {
     AttnPlan p = {};
     p.prompt = prompt_preferred(tokens, requests, kv_heads, head_dim, group, max_new);
-    p.main = split_shape(tokens, requests, kv_heads, head_dim, max_new * group, group, max_new, max_context, window);
+    p.main = split_shape(tokens, requests, kv_heads, head_dim, max_new * group, group, max_new, max_context, window, false);
     // The prompt kernel, and the split kernel with a workgroup a unit, give all
     // the keys of a row block to one workgroup.  Where a request may have few rows
     // (some have fewer than max_new tokens) behind more keys than prompts have,
-    // those with one row block go to the split kernel in ranges.  Us, before and
-    // after, 32 heads on 2: a prompt of 4096 and a token behind 131072 3336 / 191, one
-    // of 2048 and 63 tokens behind 8000 250 / 127, of 512 and those 451 / 86; eight
-    // chunks of up to 512 behind 15000, which gain nothing, 570 / 570.
-    const int64_t few_new = group < 32 ? 32 / group : 1;
+    // those with up to 1024 go to the split kernel in ranges.  Us, before and after,
+    // 32 heads on 2: a prompt of 4096 beside one token behind 131072 3336 / 184,
+    // beside 8 of them 3316 / 218, beside 64 3333 / 400; one of 2048 beside 63 tokens
+    // behind 8000 250 / 113; eight chunks of up to 512 behind 15000, which gain
+    // nothing, 582 / 585.
+    const int64_t few_new = group < 1024 ? 1024 / group : 1;
     const bool serial = p.prompt || p.main.groups == 0;
     if (serial && max_new > few_new && tokens < requests * max_new &&
         longest_walk(max_new, max_context, window) >= (max_new + kTile - 1) / kTile + long_walk(p.prompt, p.main.sparse)) {
-        p.few = split_shape(tokens, requests, kv_heads, head_dim, few_new * group, group, few_new, max_context, window);
+        p.few = split_shape(tokens, requests, kv_heads, head_dim, few_new * group, group, few_new, max_context, window, true);
         p.rest = p.few.groups > 0;
         p.main_least = p.rest ? (int)(few_new * group) + 1 : 0;
     }

@@ -83,17 +83,17 @@ def test_one_draft_beside_decodes_takes_no_multiple_of_the_time():
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 4000), (False, 4000), (True, 50)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_prompts_beside_tokens_behind_long_contexts(dtype, causal, window):
-    """Requests with few rows and with many in one call: up to 4 new tokens of 8
+    """Requests with few rows and with many in one call: up to 128 new tokens of 8
     heads a key head go one way, more of them the other."""
     rng = np.random.default_rng(window)
-    new, past = [450, 1, 3, 0, 200, 1, 4, 5, 1], [0, 5000, 4100, 77, 30, 0, 6000, 4500, 2]
+    new, past = [450, 1, 128, 0, 129, 1, 4, 33, 1], [0, 5000, 4100, 77, 30, 0, 6000, 4500, 2]
     compare(rng, new, [n + p for n, p in zip(new, past)], 64, 8, 32, dtype, causal=causal, window=window)
 
 
 @pytest.mark.parametrize("heads,kv,dim,tokens", [(16, 16, 64, 2100), (40, 1, 64, 1800), (64, 1, 128, 300), (48, 16, 128, 700)])
 def test_groups_of_heads_beside_long_contexts(heads, kv, dim, tokens):
     rng = np.random.default_rng(heads)
-    few = max(1, 32 // (heads // kv))
+    few = max(1, 1024 // (heads // kv))
     new = [tokens, 1, few, few + 1, 0, 1]
     past = [5, tokens + 3000, tokens + 2500, tokens + 2600, 9, 40]
     compare(rng, new, [n + p for n, p in zip(new, past)], heads, kv, 16, BF16, dim=dim, prompt=False)
@@ -122,6 +122,7 @@ def test_many_tokens_and_one_long_context(requests, heads, kv, dim):
 
 @pytest.mark.parametrize("what,heads,kv,dim,first,second", [
     ("a prompt beside one token", 32, 2, 128, ([4096], [4096]), ([1], [131072])),
+    ("a prompt beside a draft", 32, 2, 128, ([4096], [4096]), ([8], [131072])),
     ("a prompt beside 63 tokens", 32, 2, 128, ([512], [512]), ([1] * 63, [8000] * 63)),
     ("a prompt beside one token, 64 channels", 16, 16, 64, ([4096], [4096]), ([1], [131072])),
     ("a prompt beside 255 tokens, 64 channels", 16, 16, 64, ([4096], [4096]), ([1] * 255, [500] * 255)),
