@@ -40,8 +40,9 @@ struct Int {
 
 // x / s correctly rounded, from the correctly rounded inverse of s: the
 // residual of x * inverse is exact, and one step along it lands on the
-// nearest float (checked for every significand of s with every 11-bit one of
-// x and quotients of 2^-2 to 2^8; below, the code is 0 whatever the last bit).
+// nearest float (tests/test_kv_quotient.py: scales from the floor up, each with
+// every 11-bit significand of x and quotients of 2^-2 to 2^8; below, the code is
+// 0 whatever the last bit).
 // A third of a general division's instructions.
 struct Scale {
     float s, inverse; // both 0 for a run of zeros
