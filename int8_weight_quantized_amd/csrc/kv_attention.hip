@@ -119,8 +119,9 @@ __device__ __forceinline__ Request request_or_gap(const KvAttnArgs &a, int r)
 //
 // Bound by HBM: 2 * D + 8 / B bytes a key and head, read straight into
 // registers; past the caches where there is one block of query rows (ONCE:
-// 6.0 against 5.6 TB/s on long contexts), else through them (up to a fifth
-// faster: 898 -> 718 us for eight chunks of up to 512 tokens).  A
+// 6.0 against 5.6 TB/s on long contexts), else through them (64 tokens behind
+// 131072, 32 heads on 2: 260 us for 350; eight prompts of 4096, 16 heads of 64:
+// 465 for 510).  A
 // tile is D / 4 loads of 16 bytes a lane in flight; asking for the next tile
 // before this one's products gained nothing, with eight waves a CU.
 // ---------------------------------------------------------------------------

@@ -350,10 +350,13 @@ void write_block(const KvCacheArgs &a, hipStream_t stream)
 {
     // Small windows suit single tokens, which a workgroup's waves take one after
     // the other, large ones long runs, whose further windows hold nothing to do
-    // and cost a workgroup each.  With windows of 4, 16 and 64, us: 64 single
-    // tokens (2 heads of 128) 4.5, 10.6, 36, and 512 (8 heads) 14.7, 17.1, 41;
-    // 2048 (2 heads) 13.0, 15.0, 39, and one prompt of 2000 (8 heads, blocks of
-    // 16) 17.9, 6.3, 4.9; four prompts of 4000 (8 heads, blocks of 64) 166, 44, 26.
+    // and cost a workgroup each.  Which of them the slots are the host cannot see;
+    // their number says what they are likely to be, and between the two a middle
+    // window is best for neither and bad for neither.  With windows of 4, 16 and
+    // 64, us: 64 single tokens (2 heads of 128) 4.5, 10.6, 36, and 512 (8 heads) 14.7,
+    // 17.1, 41; 2048 (2 heads) 13.0, 15.0, 39, and one prompt of 2000 (8 heads,
+    // blocks of 16) 17.9, 6.3, 4.9; four prompts of 4000 (8 heads, blocks of 64) 166,
+    // 44, 26.
     if (a.tokens <= 512)
         write_window<DT, D, 4, MOST>(a, stream);
     else if (a.tokens <= 4096)

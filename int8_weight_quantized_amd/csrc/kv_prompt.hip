@@ -21,10 +21,13 @@
 // the same time one tile is read, the next is written and a third is still
 // read by the waves that come behind.  A barrier ends each phase.
 //
-// Bound by the two phases' lengths: a matrix phase is 32 instructions of 32
-// cycles and takes some 1140 cycles; in the other, for each of 32 scores a
-// lane, one FMA, one exponential, one addition and half a conversion, which
-// at 5 cycles an instruction (9 an exponential) are as many.  The staging of
+// Bound by the phases' length.  By counters (eight chunks of 512 behind 15000, 32
+// heads on 2: 512 workgroups of 242 tiles) a phase takes 1900 cycles, and a wave
+// issues a tile 32 matrix instructions of 32 cycles, 1024 in all, and 200 vector
+// ones, active for 920, beside 93 scalar and 40 LDS ones.  So one wave's products
+// and the other's softmax take nearly as long as one behind the other: the matrix
+// cores are busy 54 % of the time (42 % over prompts whose row blocks do not come
+// out even).  Why the two overlap so little has not been found.  The staging of
 // the next tile goes with the matrix phase (with the other one: 2 to 3 %
 // slower; dealt out among the matrix instructions by hand: 15 % slower).
 // Measured: four prompts of up to 8192 tokens, 32 query heads on 8 key heads,
