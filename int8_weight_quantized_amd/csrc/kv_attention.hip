@@ -751,7 +751,7 @@ SplitShape split_shape(int64_t tokens, int64_t requests, int64_t kv_heads, int64
     p.rt = rows <= 16 ? 1 : 2;
     p.units = (int)((rows + 16 * p.rt - 1) / (16 * p.rt) * kv_heads);
     p.live = (tokens * group / (16 * p.rt) + requests) * kv_heads;
-    p.sparse = requests * p.units > 2 * p.live;
+    p.sparse = requests * p.units > 2 * p.live && p.live < (1 << 23); // (a grid has fewer than 2^32 threads a side)
     const int64_t tiles = longest_walk(max_new, max_context, window);
     const int64_t gaps = 2 * (1 + kUnitCost) * (tokens * group / (16 * p.rt) + 1) * kv_heads; // tokens of no request
     const int64_t all = (tiles + kUnitCost) * requests * p.units + gaps;
