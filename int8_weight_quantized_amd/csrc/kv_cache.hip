@@ -9,9 +9,10 @@
 //   q  = clamp(round_half_even(fp32(x / S)), -127, 127)      (S = 0: 0)
 //   q_kept = round_half_even(fp32(q_kept * fp32(S_old / S))) where S > S_old
 //
-// so a block's scale is the largest value that its live tokens brought, a
-// token at offset 0 starts the block afresh, and nothing before the run is
-// read unless the scale grows.
+// so a block's scale is the largest value that tokens brought since its offset
+// 0 was written (also tokens that others have replaced since, as after rejected
+// drafts), a token at offset 0 starts the block afresh, and nothing before the
+// run is read unless the scale grows.
 //
 // Bound by HBM for prompts (2 bytes in, 1 byte out an element: 4 prompts of
 // 4000 tokens, 8 heads of 128, in 26 us, 3.8 TB/s) and by latency for single

@@ -7,7 +7,8 @@ import pytest
 torch = pytest.importorskip("torch")
 import int8_weight_quantized_amd as qw  # noqa: E402
 from gpu_util import say  # noqa: E402
-from test_gpu_kv import BF16, F16, TYPES, ints  # noqa: E402
+import kv_reference as ref  # noqa: E402
+from test_gpu_kv import BF16, F16, TYPES, dev, ints  # noqa: E402
 from test_gpu_kv_many_rows import compare  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -135,3 +136,40 @@ def test_a_long_context_is_shared_out(what, heads, kv, dim, first, second):
     both = microseconds(call_of(first[0] + second[0], first[1] + second[1], heads, kv, dim, 64))
     print("%s: %.1f and %.1f us alone, %.1f us together" % (what, one, two, both))
     assert both < 1.7 * (one + two)
+
+
+@pytest.mark.parametrize("new,past,heads,kv,dim", [
+    ([450, 1, 3, 200], [0, 5000, 4100, 30], 64, 8, 128),              # many rows, and few in ranges
+    ([2100, 1, 1024, 3], [5, 5100, 30, 4000], 16, 16, 64),            # a workgroup a unit, and few in ranges
+    ([199, 200] + [1] * 39, [10] * 41, 16, 16, 64),                   # the row blocks in a row
+    ([1] * 30 + [60], [1500] * 31, 32, 2, 128),                       # joined by ranges
+])
+def test_a_captured_call(new, past, heads, kv, dim):
+    """One graph, replayed over other queries and contexts with eager work
+    between, against the eager calls."""
+    rng = np.random.default_rng(len(new))
+    top = np.array(new) + np.array(past)
+    table, blocks = ref.pages(rng, [int(c) for c in top], 32)
+    on = [dev(c) for c in ref.random_cache(rng, blocks, kv, dim, 32)]
+    q = torch.zeros((sum(new) + 3, heads, dim), dtype=F16, device="cuda:0")
+    context, tab, cu = ints(top), ints(table), ints(np.concatenate([[0], np.cumsum(new)]))
+    steps = [(dev(rng.standard_normal(q.shape), F16), ints(np.maximum(new, top - rng.integers(0, 40, len(new))))) for _ in range(3)]
+    call = lambda: qw.kv_attention(q, *on, tab, context, cu, max(new), max_context=int(top.max()))  # noqa: E731
+    eager = []
+    for x, c in steps:
+        q.copy_(x)
+        context.copy_(c)
+        eager.append(call())
+    torch.cuda.synchronize()
+    say("a captured call of %d requests, D=%d" % (len(new), dim))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for again in range(2):
+        for (x, c), want in zip(steps, eager):
+            q.copy_(x)
+            context.copy_(c)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and not out[-3:].any()
+            (x.float() * 2).sum().item()

@@ -9,7 +9,7 @@ import int8_weight_quantized_amd as qw  # noqa: E402
 import kv_reference as ref  # noqa: E402
 from gpu_util import say  # noqa: E402
 from test_gpu_kv import TYPES, dev, host, ints, unit, within  # noqa: E402
-from test_gpu_kv_many_rows import many_rows  # noqa: E402
+from test_gpu_kv_many_rows import compare, many_rows  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,16 @@ def test_dominant_first_key(new, heads, kv, dim, block, dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_dominant_first_key_many_rows(dtype):
     sink(450, 16384 + 450, 64, 8, 128, 64, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new,heads,kv,dim,prompt", [(1, 4, 2, 64, False), (40, 4, 2, 128, False), (450, 64, 8, 128, True)])
+def test_value_scales_over_forty_powers(new, heads, kv, dim, prompt, dtype):
+    """Blocks whose value scales lie up to 2^40 apart, and one of zeros."""
+    rng = np.random.default_rng(new)
+    context = [new + 700]
+    table, blocks = ref.pages(rng, context, 16)
+    k, v, ks, vs = ref.random_cache(rng, blocks, kv, dim, 16)
+    vs *= (2.0 ** rng.uniform(-40, 0, vs.shape)).astype(np.float32)
+    vs[table[0, 5]], v[table[0, 5]] = 0, 0
+    compare(rng, [new], context, heads, kv, 16, dtype, dim=dim, table=table, cache=(k, v, ks, vs), prompt=prompt)
