@@ -601,8 +601,9 @@ QW_API qw_status qw_probe_shader_clock(uint64_t *out, void *stream);
  * ------------------------------------------------------------------------- */
 
 typedef enum qw_dtype {
-    QW_F16 = 0, /* IEEE binary16 */
-    QW_BF16 = 1 /* bfloat16 */
+    QW_F16 = 0,  /* IEEE binary16 */
+    QW_BF16 = 1, /* bfloat16 */
+    QW_F32 = 2   /* IEEE binary32: the router's logits only */
 } qw_dtype;
 
 /* May be added to `causal` of qw_kv_attention: rows of `out` that belong to no
@@ -797,6 +798,255 @@ QW_API int64_t qw_kv_attention_workspace(int64_t tokens, int64_t q_heads, int64_
                                          int64_t head_dim, int64_t block_size,
                                          int64_t table_width, int64_t requests, int64_t max_new,
                                          int64_t max_context, int64_t window);
+
+/* ---------------------------------------------------------------------------
+ * The feed-forward half of a decoder layer: what runs between its output GEMM
+ * and the next layer's QKV GEMM.
+ *
+ *   add_rms_norm -> linear (gate and up, gated) -> linear (down, residual)
+ *   add_rms_norm -> route_experts -> experts (gate and up) -> experts (down)
+ *                -> experts_combine
+ *
+ * As for the cache, lengths and indexes that live on the device are bounded by
+ * the kernels, and no call waits for the device or allocates, so all of them
+ * can be captured into a graph.  Alignment: 16 bytes, int32 arrays 4.
+ * ------------------------------------------------------------------------- */
+
+typedef enum qw_activation {
+    QW_ACT_NONE = 0,
+    QW_ACT_RELU = 1,
+    QW_ACT_GELU = 2,      /* v Phi(v), Phi the normal distribution function */
+    QW_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    QW_ACT_SILU = 4       /* v / (1 + exp(-v)) */
+} qw_activation;
+
+/*
+ * qw_add_rms_norm -- the residual's addition and the RMS norm of each row, in
+ * fp32:
+ *
+ *   h = x + residual, rounded to `dtype`             (null residual: h = x)
+ *   y = h * weight / sqrt(mean(h^2) + eps), rounded once
+ *
+ *   x, residual  [tokens][k], x_stride and residual_stride elements between
+ *                rows; residual may be null
+ *   weight       [k] of the same dtype
+ *   h            [tokens][k] with a stride of its own (written); may be x or
+ *                residual itself (same pointer and stride); null exactly where
+ *                residual is
+ *   y            [tokens][k], contiguous (written)
+ *
+ * qw_add_rms_norm_quantize -- the same with y in int8 codes, one scale a row:
+ * the operands qx and sx of qw_w8a8_gemm and qw_w8a8_linear.
+ *
+ *   S = binary16(max|y| / 127), q = clamp(round_half_even(y / S), -127, 127)
+ *   (S == 0: q = 0)
+ *
+ * with y not rounded before.  The scale and the codes come from y in fp32, so
+ * a code may be off by one where y / S lies within fp32's rounding of a half.
+ *
+ *   q       int8 [tokens][k] (written)
+ *   scales  fp16 bits [tokens] (written)
+ *
+ * Rows with values that are not finite, or above 2^60, give unspecified
+ * outputs (of that row).
+ *
+ * Errors: QW_ERROR_INVALID_VALUE (null pointer, h null with a residual or the
+ * reverse, negative size, k <= 0, a stride below k, unknown dtype, eps negative
+ * or not finite, outputs overlapping anything else than h its own input),
+ * QW_ERROR_UNSUPPORTED (k not a multiple of 16 or above QW_QUANTIZE_MAX_K, a
+ * stride not a multiple of 8 or above 2^31 - 1, tokens above 2^31 - 1),
+ * QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.  tokens == 0 is a no-op.
+ */
+QW_API qw_status qw_add_rms_norm(const void *x, int64_t x_stride, const void *residual,
+                                 int64_t residual_stride, const void *weight, int dtype,
+                                 int64_t tokens, int64_t k, double eps, void *h, int64_t h_stride,
+                                 void *y, void *stream);
+QW_API qw_status qw_add_rms_norm_quantize(const void *x, int64_t x_stride, const void *residual,
+                                          int64_t residual_stride, const void *weight, int dtype,
+                                          int64_t tokens, int64_t k, double eps, void *h,
+                                          int64_t h_stride, int8_t *q, uint16_t *scales,
+                                          void *stream);
+
+/*
+ * qw_w8a16_linear -- qw_w8a16_gemm with what follows a Linear layer in its
+ * epilogue, in fp32, rounded once:
+ *
+ *   v[i][c] = S[c] * sum_j X[i][j] * q[c][j] + bias[c]
+ *   y[i][c] = act(v[i][c])                        + residual[i][c]
+ *   y[i][c] = act(v[i][c]) * v[i][n / 2 + c]      + residual[i][c]   (gated)
+ *
+ * A gated product's weight holds the gate's n / 2 channels, then the other
+ * factor's; its y and residual have n / 2 columns.
+ *
+ *   x, q, scales, m, n, k, stream   as qw_w8a16_gemm
+ *   bias        fp16 [n], or null
+ *   activation  qw_activation
+ *   gated       0 or 1 (then n is even)
+ *   residual    fp16 [m][columns of y], or null; may be y itself
+ *   y           fp16 [m][n], gated [m][n / 2] (written)
+ *
+ * The kernels and their choice are qw_w8a16_gemm's, tuning records included.
+ * Accuracy: the sum as there, the activations within 2^-17 relative (of v for
+ * the gelus' and silu's negative tails beyond -6).
+ * qw_w8a16_linear_path forces a kernel, and for QW_PATH_MFMA with a nonzero
+ * `tile` that tile (as qw_w8a16_gemm_tile).
+ *
+ * Errors: as qw_w8a16_gemm_path, plus QW_ERROR_INVALID_VALUE for an unknown
+ * activation, gated not 0 or 1 or with an odd n, an unknown tile or one without
+ * QW_PATH_MFMA, or y overlapping bias, or residual at another place than its
+ * own, and QW_ERROR_UNSUPPORTED where a forced kernel does not take the sizes:
+ * QW_PATH_GEMV with m > 2, or gated with k > 8192, QW_PATH_MFMA gated with
+ * n * k >= 2^32.
+ */
+QW_API qw_status qw_w8a16_linear(const uint16_t *x, const int8_t *q, const uint16_t *scales,
+                                 const uint16_t *bias, int activation, int gated,
+                                 const uint16_t *residual, uint16_t *y, int64_t m, int64_t n,
+                                 int64_t k, void *stream);
+QW_API qw_status qw_w8a16_linear_path(const uint16_t *x, const int8_t *q, const uint16_t *scales,
+                                      const uint16_t *bias, int activation, int gated,
+                                      const uint16_t *residual, uint16_t *y, int64_t m, int64_t n,
+                                      int64_t k, int path, int tile, void *stream);
+
+/*
+ * qw_w8a8_linear -- the same for qw_w8a8_gemm's operands:
+ *
+ *   v[i][c] = float(sum_j QX[i][j] * Q[c][j]) * (S[c] * Sx[i]) + bias[c]
+ *
+ *   qx, sx, q, scales, m, n, k, stream   as qw_w8a8_gemm
+ *   dtype       of bias, residual and y (qw_dtype)
+ *   others as qw_w8a16_linear
+ *
+ * Errors: as qw_w8a8_gemm_path and qw_w8a16_linear_path, plus
+ * QW_ERROR_INVALID_VALUE for an unknown dtype.
+ */
+QW_API qw_status qw_w8a8_linear(const int8_t *qx, const uint16_t *sx, const int8_t *q,
+                                const uint16_t *scales, const void *bias, int activation, int gated,
+                                const void *residual, int dtype, void *y, int64_t m, int64_t n,
+                                int64_t k, void *stream);
+QW_API qw_status qw_w8a8_linear_path(const int8_t *qx, const uint16_t *sx, const int8_t *q,
+                                     const uint16_t *scales, const void *bias, int activation,
+                                     int gated, const void *residual, int dtype, void *y, int64_t m,
+                                     int64_t n, int64_t k, int path, int tile, void *stream);
+
+/* Most experts and most of them a token that qw_route_experts takes. */
+#define QW_MAX_EXPERTS 512
+#define QW_MAX_TOP_K 64
+
+/*
+ * qw_route_experts -- the experts of each token and their weights, and the
+ * entries (a token and one of its experts) listed expert by expert.
+ *
+ *   s = exp(l) / sum exp(l) (scoring 0) or 1 / (1 + exp(-l)) (scoring 1) of a
+ *       token's logits l
+ *   c = s + bias, or without a bias the order of l
+ *
+ * With groups > 1 the experts lie in groups of experts / groups neighbours; the
+ * top_groups groups with the largest scores keep theirs: a group's score is the
+ * sum of its two largest c with a bias (of its one, where it has one), else its
+ * largest c.  A token goes to its top_k experts of the largest c, with weights
+ *
+ *   w = s [/ the sum of its s]  * scale
+ *
+ * Ties go to the lowest index.  The choice and the weights are computed in
+ * binary64; the weights are rounded to binary32.  A logit (or choice) that is
+ * -infinity or NaN is no expert's: a token with fewer than top_k others has
+ * ids -1 and weights 0 in the places behind them (a row of -infinity: a token
+ * that goes nowhere).  +infinity counts as the largest finite number.
+ *
+ *   logits    [tokens][experts] of `dtype` (QW_F16, QW_BF16 or QW_F32)
+ *   bias      fp32 [experts], or null
+ *   ids       int32 [tokens][top_k] (written)
+ *   weights   fp32 [tokens][top_k] (written)
+ *   offsets   int32 [experts + 1] (written): the first entry of each expert,
+ *             then their number
+ *   rows      int32 [tokens * top_k] (written): the entries' flat indexes
+ *             token * top_k + place, ascending for each expert; -1 behind the
+ *             last
+ *   places    int32 [tokens][top_k] (written): where `rows` holds each; -1 for
+ *             an id of -1
+ *   workspace qw_route_experts_workspace() bytes
+ *
+ * Errors: QW_ERROR_INVALID_VALUE (null pointer, negative size, top_k, groups or
+ * top_groups below 1, experts not a multiple of groups, top_groups above
+ * groups, scoring or renormalize not 0 or 1, scale not finite, unknown dtype, a
+ * workspace that is too small, outputs overlapping each other or an input),
+ * QW_ERROR_UNSUPPORTED (experts above QW_MAX_EXPERTS, top_k above QW_MAX_TOP_K,
+ * groups above 64, tokens * top_k above 2^31 - 1), QW_ERROR_MISALIGNED,
+ * QW_ERROR_LAUNCH.  tokens == 0 still writes the offsets.
+ *
+ * qw_route_experts_workspace -- workspace bytes, -1 for sizes that the call
+ * rejects.
+ */
+QW_API qw_status qw_route_experts(const void *logits, int dtype, int64_t tokens, int64_t experts,
+                                  int64_t top_k, int scoring, const float *bias, int64_t groups,
+                                  int64_t top_groups, int renormalize, double scale, int32_t *ids,
+                                  float *weights, int32_t *offsets, int32_t *rows, int32_t *places,
+                                  void *workspace, int64_t workspace_bytes, void *stream);
+QW_API int64_t qw_route_experts_workspace(int64_t tokens, int64_t experts, int64_t top_k);
+
+/*
+ * qw_w8a16_experts -- qw_w8a16_linear of each entry's row with its expert's
+ * weight:
+ *
+ *   entry p of expert e, offsets[e] <= p < offsets[e + 1]:
+ *   v[p][c] = S[e][c] * sum_j X[r][j] * q[e][c][j] + bias[e][c]
+ *   y[p][c] = act(v[p][c]),  or gated  act(v[p][c]) * v[p][n / 2 + c]
+ *
+ * with r = rows[p] / top_k (gather) or r = p.  Rows of y from offsets[experts]
+ * on become zero.
+ *
+ *   x        fp16 [x_rows][k]; without gather x_rows == entries
+ *   q        int8 [experts][n][k], scales fp16 [experts][n]
+ *   bias     fp16 [experts][n], or null
+ *   offsets  int32 [experts + 1], not decreasing; taken as within [0, entries]
+ *   rows     int32 [entries] (may be null without gather); an index whose row
+ *            is not one of x counts as a row of zeros
+ *   y        fp16 [entries][n], gated [entries][n / 2] (written)
+ *
+ * Kernels: the skinny GEMM for up to 16 entries an expert on average, else the
+ * MFMA GEMM; qw_w8a16_experts_path forces either, and a tile.  Accuracy as
+ * qw_w8a16_linear.
+ *
+ * Errors: as qw_w8a16_linear_path (which has QW_PATH_SKINNY and QW_PATH_MFMA
+ * here), plus QW_ERROR_INVALID_VALUE (experts or top_k below 1, x_rows !=
+ * entries without gather, null rows with it, y overlapping offsets or rows),
+ * QW_ERROR_UNSUPPORTED (experts above QW_MAX_EXPERTS, entries above 2^31 - 1,
+ * k above QW_MFMA_MAX_K, n * k >= 2^32, with gather (x_rows + 1) * k >= 2^31,
+ * QW_PATH_SKINNY with entries above 2^19).  entries == 0 is a no-op.
+ */
+QW_API qw_status qw_w8a16_experts(const uint16_t *x, int64_t x_rows, int gather, const int8_t *q,
+                                  const uint16_t *scales, const uint16_t *bias, int activation,
+                                  int gated, const int32_t *offsets, const int32_t *rows,
+                                  int64_t entries, int64_t top_k, uint16_t *y, int64_t experts,
+                                  int64_t n, int64_t k, void *stream);
+QW_API qw_status qw_w8a16_experts_path(const uint16_t *x, int64_t x_rows, int gather,
+                                       const int8_t *q, const uint16_t *scales, const uint16_t *bias,
+                                       int activation, int gated, const int32_t *offsets,
+                                       const int32_t *rows, int64_t entries, int64_t top_k,
+                                       uint16_t *y, int64_t experts, int64_t n, int64_t k, int path,
+                                       int tile, void *stream);
+
+/*
+ * qw_experts_combine -- the sum over each token's experts, in fp32 in the order
+ * of j, rounded once:
+ *
+ *   out[t] = residual[t] + sum_j weights[t][j] * y[places[t][j]]
+ *
+ *   y         fp16 [entries][n]
+ *   places    int32 [tokens][top_k]; a place outside [0, entries) adds nothing
+ *   weights   fp32 [tokens][top_k]
+ *   residual  fp16 [tokens][n], or null; may be out itself
+ *   out       fp16 [tokens][n] (written)
+ *
+ * Errors: QW_ERROR_INVALID_VALUE (null pointer, negative size, top_k below 1,
+ * out overlapping anything else than residual at its own place),
+ * QW_ERROR_UNSUPPORTED (sizes above 2^31 - 1, tokens * n above 2^40),
+ * QW_ERROR_MISALIGNED, QW_ERROR_LAUNCH.  tokens == 0 or n == 0 is a no-op;
+ * entries == 0 leaves the residual, or zeros (y may then be null).
+ */
+QW_API qw_status qw_experts_combine(const uint16_t *y, int64_t entries, const int32_t *places,
+                                    const float *weights, int64_t tokens, int64_t top_k,
+                                    const uint16_t *residual, uint16_t *out, int64_t n, void *stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 QW_API const char *qw_status_string(qw_status status);

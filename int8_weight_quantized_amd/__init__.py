@@ -18,7 +18,10 @@ an optional percentage clip (LightSeq slide deck, "量化流程" and
 weight ("探索ChatGLM2在算能BM1684X上INT8量化部署", sections 2-4).
 
 What a decoder layer runs between its GEMMs is here too, around a paged int8
-KV cache (kv.py): kv_plan, qk_norm_rope, kv_write, kv_read, kv_attention.
+KV cache (kv.py): kv_plan, qk_norm_rope, kv_write, kv_read, kv_attention; and
+the other half of the layer (ff.py): add_rms_norm, the products with their
+epilogue w8a16_linear and w8a8_linear, and route_experts, w8a16_experts and
+experts_combine.
 """
 
 from __future__ import annotations
@@ -27,6 +30,9 @@ import ctypes
 import os
 
 from . import kv as _kv
+from . import ff as _ff
+from .ff import (ACTIVATIONS, MAX_EXPERTS, MAX_TOP_K, ExpertRoute, add_rms_norm, experts_combine, route_experts, w8a16_experts,
+                 w8a16_linear, w8a8_linear)
 from .kv import (KV_BLOCK_SIZES, KV_HEAD_DIMS, KV_PLAN_MAX_REQUESTS, KvCache, KvPlan, kv_attention,
                  kv_attention_workspace, kv_cache, kv_plan, kv_read, kv_write, qk_norm_rope)
 
@@ -137,6 +143,7 @@ def _load():
     lib.qw_probe_shader_clock.argtypes = [vp, vp]
     lib.qw_probe_shader_clock.restype = ctypes.c_int
     _kv._declare(lib)
+    _ff._declare(lib)
     lib.qw_version.argtypes = []
     lib.qw_version.restype = ctypes.c_int
     _lib_handle = lib
@@ -607,4 +614,5 @@ __all__ = ["quantize_weights", "quantize_weights_fixed_range", "quantize_weights
            "quantize_weights_outliers_raw", "w8a16_gemm_outliers_raw", "w8a16_gemm_raw", "w8a8_gemm_raw",
            "probe_stream_read_raw", "probe_shader_clock_raw", "PATHS", "LIBRARY_PATH",
            "KvCache", "KvPlan", "kv_cache", "kv_plan", "qk_norm_rope", "kv_write", "kv_read", "kv_attention",
-           "kv_attention_workspace", "KV_HEAD_DIMS", "KV_BLOCK_SIZES", "KV_PLAN_MAX_REQUESTS"]
+           "kv_attention_workspace", "add_rms_norm", "w8a16_linear", "w8a8_linear", "ExpertRoute", "route_experts", "w8a16_experts",
+           "experts_combine", "ACTIVATIONS", "MAX_EXPERTS", "MAX_TOP_K", "KV_HEAD_DIMS", "KV_BLOCK_SIZES", "KV_PLAN_MAX_REQUESTS"]

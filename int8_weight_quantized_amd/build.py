@@ -41,8 +41,16 @@ UNITS = {
     "gemv.hip": [],
     "gemm_mfma.hip": [],
     "gemm_skinny.hip": [],
+    "linear_w8a16.hip": [],
+    "linear_w8a8.hip": [],
+    "linear_skinny.hip": [],
+    "experts_w8a16.hip": [],
     "tune.hip": [],
     "probe.hip": [],
+    "ff_api.hip": [],
+    "add_rms_norm.hip": [],
+    "route_experts.hip": [],
+    "experts_combine.hip": [],
     "kv_api.hip": [],
     "kv_plan.hip": [],
     "qk_norm_rope.hip": [],

@@ -1,0 +1,382 @@
+// ff_api.hip -- the C ABI of the feed-forward operators: argument checks on the
+// host, kernel selection, launch on the caller's stream.  Nothing is allocated
+// here, and a rejected call launches nothing and writes nothing.
+#include <math.h>
+#include <stdint.h>
+
+#include "ff_internal.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffffff;
+
+bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+bool meet(const void *a, uint64_t na, const void *b, uint64_t nb)
+{
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return a && b && na && nb && pa < pb + nb && pb < pa + na;
+}
+
+qw_status status_of(hipError_t e) { return e == hipSuccess ? QW_SUCCESS : QW_ERROR_LAUNCH; }
+
+bool known_tile(int tile, bool a8)
+{
+    return tile == 256256 || tile == 256128 || tile == 256064 || (tile == 128128 && !a8) || tile == 128064;
+}
+
+// The kernel and tile of a linear call: a tuning record of the plain product's
+// bucket, else its rule, where the kernel takes the sizes.
+void choose(const qw::LinearArgs &a, int &path, int &tile)
+{
+    const bool a8 = a.sx != nullptr;
+    const int tuned = qw::tuned_choice(a.m, a.n, a.k, a8);
+    path = tuned >= 0 ? tuned / qw::kChoicePath : qw::auto_path(a.m, a.n, a.k);
+    tile = tuned >= 0 ? tuned % qw::kChoicePath : 0;
+    if (path == QW_PATH_GEMV && (a8 || !qw::gemv_linear_supported(a.m, a.k, a.gated)))
+        path = QW_PATH_SKINNY;
+    if (path == QW_PATH_SKINNY && a.m > 16 * 65535)
+        path = QW_PATH_MFMA;
+    if (path == QW_PATH_MFMA && !qw::mfma_linear_supported(a.n, a.k, a.gated))
+        path = QW_PATH_SKINNY;
+    if (path != QW_PATH_MFMA || (tile == 256256 && a.k > qw::kPingPongMaxK) || !known_tile(tile, a8))
+        tile = 0;
+}
+
+qw_status linear(qw::LinearArgs a, int dtype, int gated, int path, int tile, void *stream)
+{
+    const bool a8 = a.sx != nullptr;
+    if (path != QW_PATH_AUTO && path != QW_PATH_MFMA && path != QW_PATH_SKINNY && (a8 || path != QW_PATH_GEMV))
+        return QW_ERROR_INVALID_VALUE;
+    if (tile != 0 && (path != QW_PATH_MFMA || !known_tile(tile, a8)))
+        return QW_ERROR_INVALID_VALUE;
+    if (a.m < 0 || a.n < 0 || a.k <= 0 || (gated != 0 && gated != 1) || (gated && a.n % 2) ||
+        a.ep.activation < QW_ACT_NONE || a.ep.activation > QW_ACT_SILU || (dtype != QW_F16 && dtype != QW_BF16))
+        return QW_ERROR_INVALID_VALUE;
+    if (a.m == 0 || a.n == 0)
+        return QW_SUCCESS;
+    if (!a.x || !a.q || !a.scales || !a.y)
+        return QW_ERROR_INVALID_VALUE;
+    if (a.k % 16 != 0 || a.m > kMaxDim || a.n > kMaxDim || a.k > (a8 ? (int64_t)QW_W8A8_MAX_K : kMaxDim))
+        return QW_ERROR_UNSUPPORTED;
+    if (off16(a.x) || off16(a.sx) || off16(a.q) || off16(a.scales) || off16(a.ep.bias) || off16(a.ep.residual) || off16(a.y))
+        return QW_ERROR_MISALIGNED;
+    a.gated = gated != 0;
+    a.ep.bf16 = dtype == QW_BF16;
+    const uint64_t m = (uint64_t)a.m, n = (uint64_t)a.n, k = (uint64_t)a.k;
+    const uint64_t ybytes = m * (gated ? n / 2 : n) * 2u;
+    if (meet(a.y, ybytes, a.x, m * k * (a8 ? 1u : 2u)) || meet(a.y, ybytes, a.sx, m * 2u) || meet(a.y, ybytes, a.q, n * k) ||
+        meet(a.y, ybytes, a.scales, n * 2u) || meet(a.y, ybytes, a.ep.bias, n * 2u) ||
+        (a.ep.residual != a.y && meet(a.y, ybytes, a.ep.residual, ybytes)))
+        return QW_ERROR_INVALID_VALUE;
+    if (path == QW_PATH_AUTO)
+        choose(a, path, tile);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (path == QW_PATH_GEMV) {
+        if (!qw::gemv_linear_supported(a.m, a.k, a.gated))
+            return QW_ERROR_UNSUPPORTED;
+        return status_of(qw::launch_gemv_linear(static_cast<const uint16_t *>(a.x), a.q, a.scales, a.ep, a.gated, a.y, a.m, a.n,
+                                                a.k, s));
+    }
+    if (path == QW_PATH_SKINNY) {
+        if (a.m > 16 * 65535)
+            return QW_ERROR_UNSUPPORTED;
+        return status_of(qw::launch_skinny_linear(a, s));
+    }
+    if (!qw::mfma_linear_supported(a.n, a.k, a.gated) || (tile == 256256 && a.k > qw::kPingPongMaxK))
+        return QW_ERROR_UNSUPPORTED;
+    if (tile == 0)
+        tile = a8 ? qw::w8a8_tile_choice(a.m, a.n, a.k) : qw::mfma_tile_choice(a.m, a.n, a.k);
+    return status_of(a8 ? qw::launch_mfma_linear_a8(tile, a, s) : qw::launch_mfma_linear(tile, a, s));
+}
+
+struct Span {
+    const void *p;
+    uint64_t n;
+};
+bool meet(Span a, Span b) { return meet(a.p, a.n, b.p, b.n); }
+
+// Rows of k 16-bit elements, `stride` apart.
+Span rows_of(const void *p, int64_t stride, int64_t k, int64_t count)
+{
+    return {p, (uint64_t)((count - 1) * stride + k) * 2u};
+}
+
+// Whether rows share an element: rows of one stride may lie between each other
+// (the columns of one matrix).
+bool rows_meet(const void *a, int64_t a_stride, const void *b, int64_t b_stride, int64_t k, int64_t count)
+{
+    if (!meet(rows_of(a, a_stride, k, count), rows_of(b, b_stride, k, count)))
+        return false;
+    if (a_stride != b_stride)
+        return true;
+    const int64_t bytes = a_stride * 2;
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    const int64_t shift = ((d % bytes) + bytes) % bytes; // b's column from a's
+    return shift < k * 2 || shift + k * 2 > bytes;
+}
+
+qw_status add_norm(qw::AddNormArgs a, int dtype, double eps, bool codes, void *stream)
+{
+    if ((dtype != QW_F16 && dtype != QW_BF16) || a.tokens < 0 || a.k <= 0 || !(eps >= 0.0) || !isfinite(eps))
+        return QW_ERROR_INVALID_VALUE;
+    if ((a.residual == nullptr) != (a.h == nullptr) && a.tokens > 0)
+        return QW_ERROR_INVALID_VALUE;
+    if (a.tokens == 0)
+        return QW_SUCCESS;
+    const bool added = a.residual != nullptr;
+    if (!added)
+        a.residual_stride = a.h_stride = a.x_stride;
+    if (!a.x || !a.weight || (codes ? !a.q || !a.scales : !a.y) || a.x_stride < a.k || a.residual_stride < a.k ||
+        a.h_stride < a.k)
+        return QW_ERROR_INVALID_VALUE;
+    if (a.k % 16 != 0 || a.k > QW_QUANTIZE_MAX_K || a.tokens > kMaxDim || a.x_stride % 8 || a.residual_stride % 8 ||
+        a.h_stride % 8 || a.x_stride > kMaxDim || a.residual_stride > kMaxDim || a.h_stride > kMaxDim)
+        return QW_ERROR_UNSUPPORTED;
+    if (off16(a.x) || off16(a.residual) || off16(a.weight) || off16(a.h) || off16(a.y) || off16(a.q) || off16(a.scales))
+        return QW_ERROR_MISALIGNED;
+    const int64_t T = a.tokens, k = a.k;
+    const Span weight = {a.weight, (uint64_t)k * 2u}, x = rows_of(a.x, a.x_stride, k, T);
+    const Span res = added ? rows_of(a.residual, a.residual_stride, k, T) : Span{nullptr, 0};
+    const Span h = added ? rows_of(a.h, a.h_stride, k, T) : Span{nullptr, 0};
+    const Span out = codes ? Span{a.q, (uint64_t)T * (uint64_t)k} : Span{a.y, (uint64_t)T * (uint64_t)k * 2u};
+    const Span scales = codes ? Span{a.scales, (uint64_t)T * 2u} : Span{nullptr, 0};
+    if (meet(out, x) || meet(out, res) || meet(out, weight) || meet(out, h) || meet(out, scales) || meet(scales, x) ||
+        meet(scales, res) || meet(scales, weight) || meet(scales, h) || meet(h, weight))
+        return QW_ERROR_INVALID_VALUE;
+    if (added) {
+        const bool on_x = a.h == a.x && a.h_stride == a.x_stride;
+        const bool on_res = a.h == a.residual && a.h_stride == a.residual_stride;
+        if ((!on_x && rows_meet(a.h, a.h_stride, a.x, a.x_stride, k, T)) ||
+            (!on_res && rows_meet(a.h, a.h_stride, a.residual, a.residual_stride, k, T)))
+            return QW_ERROR_INVALID_VALUE;
+    }
+    a.eps = (float)eps;
+    return status_of(qw::launch_add_rms_norm(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+bool route_sizes_ok(int64_t tokens, int64_t experts, int64_t top_k)
+{
+    return experts <= QW_MAX_EXPERTS && top_k <= QW_MAX_TOP_K && tokens <= kMaxDim / top_k;
+}
+
+int64_t route_blocks(int64_t tokens)
+{
+    const int64_t per = qw::route_tokens_a_block(tokens);
+    return (tokens + per - 1) / per;
+}
+
+int64_t route_workspace(int64_t tokens, int64_t experts) { return route_blocks(tokens) * experts * 4; }
+
+} // namespace
+
+extern "C" {
+
+QW_API qw_status qw_add_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                                 const void *weight, int dtype, int64_t tokens, int64_t k, double eps, void *h,
+                                 int64_t h_stride, void *y, void *stream)
+{
+    qw::AddNormArgs a = {};
+    a.x = static_cast<const uint16_t *>(x);
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.weight = static_cast<const uint16_t *>(weight);
+    a.h = static_cast<uint16_t *>(h);
+    a.y = static_cast<uint16_t *>(y);
+    a.x_stride = x_stride;
+    a.residual_stride = residual_stride;
+    a.h_stride = h_stride;
+    a.tokens = tokens;
+    a.k = k;
+    return add_norm(a, dtype, eps, false, stream);
+}
+
+QW_API qw_status qw_add_rms_norm_quantize(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                                          const void *weight, int dtype, int64_t tokens, int64_t k, double eps, void *h,
+                                          int64_t h_stride, int8_t *q, uint16_t *scales, void *stream)
+{
+    qw::AddNormArgs a = {};
+    a.x = static_cast<const uint16_t *>(x);
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.weight = static_cast<const uint16_t *>(weight);
+    a.h = static_cast<uint16_t *>(h);
+    a.q = q;
+    a.scales = scales;
+    a.x_stride = x_stride;
+    a.residual_stride = residual_stride;
+    a.h_stride = h_stride;
+    a.tokens = tokens;
+    a.k = k;
+    return add_norm(a, dtype, eps, true, stream);
+}
+
+QW_API int64_t qw_route_experts_workspace(int64_t tokens, int64_t experts, int64_t top_k)
+{
+    if (tokens < 0 || experts < 1 || top_k < 1 || !route_sizes_ok(tokens, experts, top_k))
+        return -1;
+    return route_workspace(tokens, experts);
+}
+
+QW_API qw_status qw_route_experts(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t top_k, int scoring,
+                                  const float *bias, int64_t groups, int64_t top_groups, int renormalize, double scale,
+                                  int32_t *ids, float *weights, int32_t *offsets, int32_t *rows, int32_t *places,
+                                  void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (tokens < 0 || experts < 1 || top_k < 1 || groups < 1 || top_groups < 1 || top_groups > groups || experts % groups ||
+        (scoring != 0 && scoring != 1) || (renormalize != 0 && renormalize != 1) || !isfinite(scale) ||
+        (dtype != QW_F16 && dtype != QW_BF16 && dtype != QW_F32) || workspace_bytes < 0 || !offsets)
+        return QW_ERROR_INVALID_VALUE;
+    if (tokens > 0 && (!logits || !ids || !weights || !rows || !places || !workspace))
+        return QW_ERROR_INVALID_VALUE;
+    if (!route_sizes_ok(tokens, experts, top_k) || groups > 64)
+        return QW_ERROR_UNSUPPORTED;
+    if (workspace_bytes < route_workspace(tokens, experts))
+        return QW_ERROR_INVALID_VALUE;
+    if (off16(logits) || off16(bias) || off16(workspace) || off4(ids) || off4(weights) || off4(offsets) || off4(rows) ||
+        off4(places))
+        return QW_ERROR_MISALIGNED;
+    const uint64_t entries = (uint64_t)tokens * (uint64_t)top_k * 4u;
+    const Span in[2] = {{logits, (uint64_t)tokens * (uint64_t)experts * (dtype == QW_F32 ? 4u : 2u)},
+                        {bias, (uint64_t)experts * 4u}};
+    const Span out[6] = {{ids, entries}, {weights, entries}, {rows, entries}, {places, entries},
+                         {offsets, (uint64_t)(experts + 1) * 4u}, {workspace, (uint64_t)workspace_bytes}};
+    for (int i = 0; i < 6; ++i) {
+        if (meet(out[i], in[0]) || meet(out[i], in[1]))
+            return QW_ERROR_INVALID_VALUE;
+        for (int j = i + 1; j < 6; ++j)
+            if (meet(out[i], out[j]))
+                return QW_ERROR_INVALID_VALUE;
+    }
+    qw::RouteArgs a = {};
+    a.logits = logits;
+    a.bias = bias;
+    a.tokens = tokens;
+    a.experts = (int)experts;
+    a.top_k = (int)top_k;
+    a.sigmoid = scoring;
+    a.groups = (int)groups;
+    a.top_groups = (int)top_groups;
+    a.renormalize = renormalize;
+    a.scale = (float)scale;
+    a.ids = ids;
+    a.weights = weights;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.places = places;
+    a.counts = static_cast<int32_t *>(workspace);
+    a.tokens_a_block = (int)qw::route_tokens_a_block(tokens);
+    a.blocks = (int)route_blocks(tokens);
+    return status_of(qw::launch_route_experts(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+QW_API qw_status qw_w8a16_experts_path(const uint16_t *x, int64_t x_rows, int gather, const int8_t *q, const uint16_t *scales,
+                                       const uint16_t *bias, int activation, int gated, const int32_t *offsets,
+                                       const int32_t *rows, int64_t entries, int64_t top_k, uint16_t *y, int64_t experts,
+                                       int64_t n, int64_t k, int path, int tile, void *stream)
+{
+    if ((path != QW_PATH_AUTO && path != QW_PATH_SKINNY && path != QW_PATH_MFMA) ||
+        (tile != 0 && (path != QW_PATH_MFMA || !known_tile(tile, false))))
+        return QW_ERROR_INVALID_VALUE;
+    if (x_rows < 0 || entries < 0 || n < 0 || k <= 0 || experts < 1 || top_k < 1 || (gather != 0 && gather != 1) ||
+        (!gather && x_rows != entries) || (gated != 0 && gated != 1) || (gated && n % 2) || activation < QW_ACT_NONE ||
+        activation > QW_ACT_SILU)
+        return QW_ERROR_INVALID_VALUE;
+    if (entries == 0 || n == 0)
+        return QW_SUCCESS;
+    if ((!x && x_rows > 0) || !q || !scales || !offsets || (gather && !rows) || !y)
+        return QW_ERROR_INVALID_VALUE;
+    if (k % 16 != 0 || experts > QW_MAX_EXPERTS || entries > kMaxDim || x_rows > kMaxDim || n > kMaxDim || top_k > kMaxDim ||
+        k > QW_MFMA_MAX_K || n * k >= int64_t(1) << 32 || (gather && (x_rows + 1) * k >= int64_t(1) << 31) ||
+        (path == QW_PATH_SKINNY && entries > (1 << 19)) || (tile == 256256 && k > qw::kPingPongMaxK))
+        return QW_ERROR_UNSUPPORTED;
+    if (off16(x) || off16(q) || off16(scales) || off16(bias) || off16(y) || off4(offsets) || off4(rows))
+        return QW_ERROR_MISALIGNED;
+    const uint64_t E = (uint64_t)experts, un = (uint64_t)n, uk = (uint64_t)k;
+    const Span out = {y, (uint64_t)entries * (gated ? un / 2 : un) * 2u};
+    if (meet(out, {x, (uint64_t)x_rows * uk * 2u}) || meet(out, {q, E * un * uk}) || meet(out, {scales, E * un * 2u}) ||
+        meet(out, {bias, E * un * 2u}) || meet(out, {offsets, (E + 1) * 4u}) || meet(out, {rows, (uint64_t)entries * 4u}))
+        return QW_ERROR_INVALID_VALUE;
+    const qw::LinearArgs a = {x, nullptr, q, scales, {bias, nullptr, activation, 0}, gated != 0, y, entries, n, k};
+    const qw::Experts ex = {offsets, gather ? rows : nullptr, (int)experts, (int)entries, (int)x_rows, (int)top_k};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (path == QW_PATH_AUTO)
+        path = entries <= 16 * experts && entries <= (1 << 19) ? QW_PATH_SKINNY : QW_PATH_MFMA;
+    if (path == QW_PATH_SKINNY)
+        return status_of(qw::launch_skinny_experts(a, ex, s));
+    if (tile == 0) {
+        const int64_t mean = entries / experts;
+        tile = mean >= 192 && k <= qw::kPingPongMaxK ? 256256 : mean >= 96 ? 256128 : mean >= 48 ? 256064 : 128064;
+    }
+    return status_of(qw::launch_mfma_experts(tile, a, ex, s));
+}
+
+QW_API qw_status qw_w8a16_experts(const uint16_t *x, int64_t x_rows, int gather, const int8_t *q, const uint16_t *scales,
+                                  const uint16_t *bias, int activation, int gated, const int32_t *offsets,
+                                  const int32_t *rows, int64_t entries, int64_t top_k, uint16_t *y, int64_t experts, int64_t n,
+                                  int64_t k, void *stream)
+{
+    return qw_w8a16_experts_path(x, x_rows, gather, q, scales, bias, activation, gated, offsets, rows, entries, top_k, y,
+                                 experts, n, k, QW_PATH_AUTO, 0, stream);
+}
+
+QW_API qw_status qw_experts_combine(const uint16_t *y, int64_t entries, const int32_t *places, const float *weights,
+                                    int64_t tokens, int64_t top_k, const uint16_t *residual, uint16_t *out, int64_t n,
+                                    void *stream)
+{
+    if (entries < 0 || tokens < 0 || top_k < 1 || n < 0)
+        return QW_ERROR_INVALID_VALUE;
+    if (tokens == 0 || n == 0)
+        return QW_SUCCESS;
+    if ((!y && entries > 0) || !places || !weights || !out)
+        return QW_ERROR_INVALID_VALUE;
+    if (entries > kMaxDim || tokens > kMaxDim || top_k > kMaxDim || n > kMaxDim || tokens > (int64_t(1) << 40) / n)
+        return QW_ERROR_UNSUPPORTED;
+    if (off16(y) || off16(residual) || off16(out) || off4(places) || off4(weights))
+        return QW_ERROR_MISALIGNED;
+    const uint64_t t = (uint64_t)tokens, un = (uint64_t)n;
+    const Span to = {out, t * un * 2u};
+    if (meet(to, {y, (uint64_t)entries * un * 2u}) || meet(to, {places, t * (uint64_t)top_k * 4u}) ||
+        meet(to, {weights, t * (uint64_t)top_k * 4u}) || (residual != out && meet(to, {residual, t * un * 2u})))
+        return QW_ERROR_INVALID_VALUE;
+    const qw::CombineArgs a = {y, places, weights, residual, out, tokens, entries, n, (int)top_k};
+    return status_of(qw::launch_experts_combine(a, static_cast<hipStream_t>(stream)));
+}
+
+QW_API qw_status qw_w8a16_linear_path(const uint16_t *x, const int8_t *q, const uint16_t *scales, const uint16_t *bias,
+                                      int activation, int gated, const uint16_t *residual, uint16_t *y, int64_t m,
+                                      int64_t n, int64_t k, int path, int tile, void *stream)
+{
+    const qw::LinearArgs a = {x, nullptr, q, scales, {bias, residual, activation, 0}, false, y, m, n, k};
+    return linear(a, QW_F16, gated, path, tile, stream);
+}
+
+QW_API qw_status qw_w8a16_linear(const uint16_t *x, const int8_t *q, const uint16_t *scales, const uint16_t *bias,
+                                 int activation, int gated, const uint16_t *residual, uint16_t *y, int64_t m, int64_t n,
+                                 int64_t k, void *stream)
+{
+    return qw_w8a16_linear_path(x, q, scales, bias, activation, gated, residual, y, m, n, k, QW_PATH_AUTO, 0, stream);
+}
+
+QW_API qw_status qw_w8a8_linear_path(const int8_t *qx, const uint16_t *sx, const int8_t *q, const uint16_t *scales,
+                                     const void *bias, int activation, int gated, const void *residual, int dtype, void *y,
+                                     int64_t m, int64_t n, int64_t k, int path, int tile, void *stream)
+{
+    if (!sx && m != 0 && n != 0)
+        return QW_ERROR_INVALID_VALUE;
+    // (sx also says which product this is, and the empty ones may have none)
+    static const uint16_t empty = 0;
+    const qw::LinearArgs a = {qx, sx ? sx : &empty, q, scales,
+                              {static_cast<const uint16_t *>(bias), static_cast<const uint16_t *>(residual), activation, 0},
+                              false, static_cast<uint16_t *>(y), m, n, k};
+    return linear(a, dtype, gated, path, tile, stream);
+}
+
+QW_API qw_status qw_w8a8_linear(const int8_t *qx, const uint16_t *sx, const int8_t *q, const uint16_t *scales,
+                                const void *bias, int activation, int gated, const void *residual, int dtype, void *y,
+                                int64_t m, int64_t n, int64_t k, void *stream)
+{
+    return qw_w8a8_linear_path(qx, sx, q, scales, bias, activation, gated, residual, dtype, y, m, n, k, QW_PATH_AUTO, 0,
+                               stream);
+}
+
+} // extern "C"

@@ -25,6 +25,7 @@
 // LDS layout of X: [m][chunk][half h][lane] x 16 bytes, where entry
 // (m, c, h, l) holds x[m][c*1024 + 16 l + 8 h .. +7].  Lane l reads
 // consecutive 16-byte slots for h = 0 and h = 1: no bank conflicts.
+#include "epilogue_device.h"
 #include "qw_device.h"
 #include "qw_internal.h"
 
@@ -44,12 +45,14 @@ struct GemvItem {
     u32x4_t w[RU][CH];
 };
 
-template <int MT, int RU, int CH>
+// EPI: kLinear adds the epilogue of qw_w8a16_linear (no zero points or lists).
+template <int MT, int RU, int CH, int EPI>
 __global__ __launch_bounds__(kGemvThreads) void gemv_kernel(
     const uint16_t *__restrict__ x, const int8_t *__restrict__ q,
     const uint16_t *__restrict__ scales, const int8_t *__restrict__ zeros, OutlierList ol,
-    uint16_t *__restrict__ y, int m, int n, int k, int chunks, int total_waves)
+    uint16_t *__restrict__ y, int m, int n, int k, int chunks, int total_waves, Epilogue ep)
 {
+    static_assert(EPI != kGated, "not built");
     extern __shared__ u32x4_t xs[];
     const int tid = threadIdx.x;
     const int lane = __lane_id();
@@ -165,9 +168,14 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_kernel(
                 if (j < my_rows && mm < m) {
                     const float s = f16_bits_to_f32(scales[row]);
                     float out = acc[0] * s;
+                    if constexpr (EPI != kPlain) {
+                        out = activate(ep.activation, out + (ep.bias ? f16_bits_to_f32(ep.bias[row]) : 0.0f));
+                        if (ep.residual)
+                            out += f16_bits_to_f32(ep.residual[(int64_t)mm * n + row]);
+                    }
                     // exact outliers of this row, with X from the LDS copy
                     // (entry e holds x[mm][c kChunkK + 16 l + 8 h + 0..7])
-                    if (ol.idx != nullptr) {
+                    if (EPI == kPlain && ol.idx != nullptr) {
                         const _Float16 *xh = reinterpret_cast<const _Float16 *>(xs);
                         for (int e = 0; e < ol.cap; ++e) {
                             const int kk = ol.idx[row * ol.cap + e];
@@ -194,10 +202,10 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_kernel(
     }
 }
 
-template <int MT, int RU, int CH, int WPC>
+template <int MT, int RU, int CH, int WPC, int EPI = kPlain>
 hipError_t launch_cfg(const uint16_t *x, const int8_t *q, const uint16_t *scales, const int8_t *zeros,
                       OutlierList ol, uint16_t *y,
-                      int64_t m, int64_t n, int64_t k, hipStream_t stream)
+                      int64_t m, int64_t n, int64_t k, hipStream_t stream, Epilogue ep = {})
 {
     const int chunks = (int)((k + kChunkK - 1) / kChunkK);
     const size_t lds = (size_t)MT * chunks * 2 * kWave * sizeof(u32x4_t);
@@ -216,8 +224,8 @@ hipError_t launch_cfg(const uint16_t *x, const int8_t *q, const uint16_t *scales
         waves = (groups + per - 1) / per;
     }
     const int blocks = (int)((waves + kGemvWaves - 1) / kGemvWaves);
-    hipLaunchKernelGGL((gemv_kernel<MT, RU, CH>), dim3(blocks), dim3(kGemvThreads), lds, stream,
-                       x, q, scales, zeros, ol, y, (int)m, (int)n, (int)k, chunks, (int)waves);
+    hipLaunchKernelGGL((gemv_kernel<MT, RU, CH, EPI>), dim3(blocks), dim3(kGemvThreads), lds, stream,
+                       x, q, scales, zeros, ol, y, (int)m, (int)n, (int)k, chunks, (int)waves, ep);
     return hipGetLastError();
 }
 
@@ -251,14 +259,19 @@ hipError_t launch_cfg(const uint16_t *x, const int8_t *q, const uint16_t *scales
 // fp16 rounding of Y.
 // ---------------------------------------------------------------------------
 
+// EPI: the epilogue of qw_w8a16_linear (no zero points or lists).  A gated
+// product's wave takes columns of Y: its row 2 t is the gate's of column t and
+// row 2 t + 1 the other factor's, whose step finishes both.
 constexpr int kStreamMaxChunks = 8; // k <= 8192: X takes 8 VGPRs per chunk and row
 constexpr int kStreamWavesPerCu = 8;
 
-template <int MT, int CH, bool ZP>
+template <int MT, int CH, bool ZP, int EPI>
 __global__ __launch_bounds__(256) void gemv_stream_kernel(
     const uint16_t *__restrict__ x, const int8_t *__restrict__ q, const uint16_t *__restrict__ scales,
-    const int8_t *__restrict__ zeros, OutlierList ol, uint16_t *__restrict__ y, int m, int n, int k, int waves)
+    const int8_t *__restrict__ zeros, OutlierList ol, uint16_t *__restrict__ y, int m, int n, int k, int waves,
+    Epilogue ep)
 {
+    const int n_out = EPI == kGated ? n / 2 : n;
     const int lane = __lane_id();
     const int gw = blockIdx.x * kGemvWaves + threadIdx.x / kWave;
     if (gw >= waves)
@@ -302,13 +315,17 @@ __global__ __launch_bounds__(256) void gemv_stream_kernel(
             }
     }
     constexpr int R = MT; // partial sums per row: one per activation row
-    const int rows = (n - 1 - gw) / waves + 1;
+    const int columns = (n_out - 1 - gw) / waves + 1;
+    const int rows = EPI == kGated ? 2 * columns : columns;
+    auto row_of = [&](int t) -> int64_t {
+        return EPI == kGated ? gw + (int64_t)(t >> 1) * waves + (t & 1) * n_out : gw + (int64_t)t * waves;
+    };
     const int mine = butterfly_index<R>(lane); // the activation row this lane writes (R > 1)
     // a row in flight: its codes, and its scale and zero point (loaded with
     // the codes, so that the epilogue does not wait for another load)
     struct Row {
         u32x4_t w[CH];
-        uint16_t s;
+        uint16_t s, b;
         int8_t z;
     };
     // Lanes past the end of a ragged last chunk load the row's last 16
@@ -319,16 +336,19 @@ __global__ __launch_bounds__(256) void gemv_stream_kernel(
     for (int c = 0; c < CH; ++c)
         koff[c] = min(c * kChunkK + lane * 16, k - 16);
     auto issue = [&](int t, Row &b) {
-        const int8_t *qr = q + (gw + (int64_t)t * waves) * k;
-        const int64_t row = gw + (int64_t)t * waves;
+        const int64_t row = row_of(t);
+        const int8_t *qr = q + row * k;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
             b.w[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(qr + koff[c]));
         b.s = scales[row];
+        if constexpr (EPI != kPlain)
+            b.b = ep.bias ? ep.bias[row] : (uint16_t)0;
         b.z = ZP ? zeros[row] : (int8_t)0;
     };
+    float gate = 0.0f; // kGated: the activated first factor of the column in hand
     auto consume = [&](int t, const Row &b) {
-        const int64_t row = gw + (int64_t)t * waves;
+        const int64_t row = row_of(t);
         float acc[R];
 #pragma unroll
         for (int mm = 0; mm < MT; ++mm)
@@ -359,6 +379,23 @@ __global__ __launch_bounds__(256) void gemv_stream_kernel(
         butterfly_reduce<R>(acc);
         if ((lane & (kWave / R - 1)) == 0 && mine < m) {
             float out = acc[0] * f16_bits_to_f32(b.s);
+            if constexpr (EPI != kPlain) {
+                const int64_t at = (int64_t)mine * n_out + (EPI == kGated ? row - n_out : row);
+                out += f16_bits_to_f32(b.b);
+                if constexpr (EPI == kGated) {
+                    if (!(t & 1)) {
+                        gate = activate(ep.activation, out);
+                        return;
+                    }
+                    out *= gate;
+                } else {
+                    out = activate(ep.activation, out);
+                }
+                if (ep.residual)
+                    out += f16_bits_to_f32(ep.residual[at]);
+                y[at] = f32_to_f16_bits(out);
+                return;
+            }
             // exact outliers of this row, with X read from global memory
             if (ol.idx != nullptr) {
                 for (int e = 0; e < ol.cap; ++e) {
@@ -400,35 +437,44 @@ __global__ __launch_bounds__(256) void gemv_stream_kernel(
 
 template <int MT, int CH>
 hipError_t launch_stream(const uint16_t *x, const int8_t *q, const uint16_t *scales, const int8_t *zeros,
-                         OutlierList ol, uint16_t *y, int64_t m, int64_t n, int64_t k, hipStream_t stream)
+                         OutlierList ol, uint16_t *y, int64_t m, int64_t n, int64_t k, hipStream_t stream, int epi,
+                         Epilogue ep)
 {
     // about 8 waves per CU, trimmed so that every wave walks the same number of rows
-    int64_t waves = std::min<int64_t>(n, (int64_t)device_cu_count() * kStreamWavesPerCu);
-    const int64_t per = (n + waves - 1) / waves;
-    waves = (n + per - 1) / per;
+    const int64_t columns = epi == kGated ? n / 2 : n;
+    int64_t waves = std::min<int64_t>(columns, (int64_t)device_cu_count() * kStreamWavesPerCu);
+    const int64_t per = (columns + waves - 1) / waves;
+    waves = (columns + per - 1) / per;
     const int blocks = (int)((waves + kGemvWaves - 1) / kGemvWaves);
-    if (zeros == nullptr)
-        hipLaunchKernelGGL((gemv_stream_kernel<MT, CH, false>), dim3(blocks), dim3(kGemvThreads), 0, stream, x, q,
-                           scales, zeros, ol, y, (int)m, (int)n, (int)k, (int)waves);
+#define QW_STREAM_LAUNCH(Z, E)                                                                                     \
+    hipLaunchKernelGGL((gemv_stream_kernel<MT, CH, Z, E>), dim3(blocks), dim3(kGemvThreads), 0, stream, x, q, scales, \
+                       zeros, ol, y, (int)m, (int)n, (int)k, (int)waves, ep)
+    if (epi == kGated)
+        QW_STREAM_LAUNCH(false, kGated);
+    else if (epi == kLinear)
+        QW_STREAM_LAUNCH(false, kLinear);
+    else if (zeros == nullptr)
+        QW_STREAM_LAUNCH(false, kPlain);
     else
-        hipLaunchKernelGGL((gemv_stream_kernel<MT, CH, true>), dim3(blocks), dim3(kGemvThreads), 0, stream, x, q,
-                           scales, zeros, ol, y, (int)m, (int)n, (int)k, (int)waves);
+        QW_STREAM_LAUNCH(true, kPlain);
+#undef QW_STREAM_LAUNCH
     return hipGetLastError();
 }
 
 template <int MT>
 hipError_t launch_stream_chunks(const uint16_t *x, const int8_t *q, const uint16_t *scales, const int8_t *zeros,
-                                OutlierList ol, uint16_t *y, int64_t m, int64_t n, int64_t k, hipStream_t stream)
+                                OutlierList ol, uint16_t *y, int64_t m, int64_t n, int64_t k, hipStream_t stream,
+                                int epi = kPlain, Epilogue ep = {})
 {
     switch ((k + kChunkK - 1) / kChunkK) {
-    case 1: return launch_stream<MT, 1>(x, q, scales, zeros, ol, y, m, n, k, stream);
-    case 2: return launch_stream<MT, 2>(x, q, scales, zeros, ol, y, m, n, k, stream);
-    case 3: return launch_stream<MT, 3>(x, q, scales, zeros, ol, y, m, n, k, stream);
-    case 4: return launch_stream<MT, 4>(x, q, scales, zeros, ol, y, m, n, k, stream);
-    case 5: return launch_stream<MT, 5>(x, q, scales, zeros, ol, y, m, n, k, stream);
-    case 6: return launch_stream<MT, 6>(x, q, scales, zeros, ol, y, m, n, k, stream);
-    case 7: return launch_stream<MT, 7>(x, q, scales, zeros, ol, y, m, n, k, stream);
-    default: return launch_stream<MT, 8>(x, q, scales, zeros, ol, y, m, n, k, stream);
+    case 1: return launch_stream<MT, 1>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
+    case 2: return launch_stream<MT, 2>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
+    case 3: return launch_stream<MT, 3>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
+    case 4: return launch_stream<MT, 4>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
+    case 5: return launch_stream<MT, 5>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
+    case 6: return launch_stream<MT, 6>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
+    case 7: return launch_stream<MT, 7>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
+    default: return launch_stream<MT, 8>(x, q, scales, zeros, ol, y, m, n, k, stream, epi, ep);
     }
 }
 
@@ -466,6 +512,24 @@ hipError_t launch_gemv(const uint16_t *x, const int8_t *q, const uint16_t *scale
     if (m <= 4)
         return launch_cfg<4, 2, 2, 16>(x, q, scales, zeros, ol, y, m, n, k, stream);
     return launch_cfg<8, 2, 2, 16>(x, q, scales, zeros, ol, y, m, n, k, stream);
+}
+
+bool gemv_linear_supported(int64_t m, int64_t k, bool gated)
+{
+    return m <= 2 && (gated ? k <= kStreamMaxChunks * kChunkK : gemv_supported(m, k));
+}
+
+hipError_t launch_gemv_linear(const uint16_t *x, const int8_t *q, const uint16_t *scales, const Epilogue &ep, bool gated,
+                              uint16_t *y, int64_t m, int64_t n, int64_t k, hipStream_t stream)
+{
+    const OutlierList none = {nullptr, nullptr, 0};
+    const int epi = gated ? kGated : kLinear;
+    if ((k + kChunkK - 1) / kChunkK <= kStreamMaxChunks)
+        return m <= 1 ? launch_stream_chunks<1>(x, q, scales, nullptr, none, y, m, n, k, stream, epi, ep)
+                      : launch_stream_chunks<2>(x, q, scales, nullptr, none, y, m, n, k, stream, epi, ep);
+    if (m <= 1)
+        return launch_cfg<1, 2, 4, 28, kLinear>(x, q, scales, nullptr, none, y, m, n, k, stream, ep);
+    return launch_cfg<2, 1, 4, 32, kLinear>(x, q, scales, nullptr, none, y, m, n, k, stream, ep);
 }
 
 } // namespace qw

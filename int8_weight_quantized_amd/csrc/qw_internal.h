@@ -32,6 +32,27 @@ constexpr int kMfmaOutlierSlots = 4;
 // Longer rows go to the skinny kernel, which indexes in 64 bits.
 constexpr int64_t kMfmaMaxK = QW_MFMA_MAX_K;
 
+// What a product's epilogue adds to acc * scale, all of it optional (EPI of
+// the kernels: kLinear, kGated): y = act(v + bias) [* (v' + bias')] + residual
+// in fp32, rounded once.  16-bit values, bf16 if `bf16`, else fp16.
+struct Epilogue {
+    const uint16_t *bias;     // [n], or null
+    const uint16_t *residual; // [m][columns of y], or null
+    int activation;           // QW_ACT_*
+    int bf16;
+};
+enum { kPlain = 0, kLinear = 1, kGated = 2 };
+
+// A grouped product (GRP of the kernels): entry p of `entries` belongs to the
+// expert e with offsets[e] <= p < offsets[e + 1], whose weight is the e-th of
+// `count`; its activation row is p, or (rows non-null) rows[p] / top_k of
+// `x_rows`.
+struct Experts {
+    const int32_t *offsets; // [count + 1]
+    const int32_t *rows;    // [entries], or null
+    int count, entries, x_rows, top_k;
+};
+
 // Activation rows the skinny kernel covers per pass over the weights (32
 // where it runs two 16-row activation tiles per wave, else 16).
 int skinny_rows_per_pass(int64_t m, int64_t k);
@@ -135,5 +156,38 @@ hipError_t launch_w8a8_gemm_tile(int tile, const int8_t *qx, const uint16_t *sx,
 hipError_t launch_mfma_gemm_tile(int tile, const uint16_t *x, const int8_t *q, const uint16_t *scales,
                                  const int8_t *zeros, OutlierList ol, uint16_t *y, int64_t m, int64_t n,
                                  int64_t k, hipStream_t stream);
+
+// Weight-tile columns per group of the MFMA GEMM's tile order, for a grid of
+// tiles_m x tiles_n of this tile.
+int mfma_tile_group(int tile, bool a8, int64_t tiles_m, int64_t tiles_n);
+
+// ---------------------------------------------------------------------------
+// The products with an epilogue (qw_w8a16_linear, qw_w8a8_linear) and the
+// experts' (qw_w8a16_experts).
+// ---------------------------------------------------------------------------
+struct LinearArgs {
+    const void *x;          // fp16 [m][k], or with sx int8
+    const uint16_t *sx;     // fp16 [m] (W8A8), or null
+    const int8_t *q;        // [n][k]; grouped: [experts][n][k]
+    const uint16_t *scales; // fp16 [n]; grouped: [experts][n]
+    Epilogue ep;
+    bool gated;
+    uint16_t *y;
+    int64_t m, n, k;
+};
+
+// The GEMV takes one or two rows; where gated, of up to 8192.
+bool gemv_linear_supported(int64_t m, int64_t k, bool gated);
+hipError_t launch_gemv_linear(const uint16_t *x, const int8_t *q, const uint16_t *scales, const Epilogue &ep, bool gated,
+                              uint16_t *y, int64_t m, int64_t n, int64_t k, hipStream_t stream);
+hipError_t launch_skinny_linear(const LinearArgs &a, hipStream_t stream);
+// Whether the MFMA kernels take these sizes, and their launch (tile as in
+// mfma_tile_choice).
+bool mfma_linear_supported(int64_t n, int64_t k, bool gated);
+hipError_t launch_mfma_linear(int tile, const LinearArgs &a, hipStream_t stream);
+hipError_t launch_mfma_linear_a8(int tile, const LinearArgs &a, hipStream_t stream);
+// Grouped: a.m entries.
+hipError_t launch_skinny_experts(const LinearArgs &a, const Experts &ex, hipStream_t stream);
+hipError_t launch_mfma_experts(int tile, const LinearArgs &a, const Experts &ex, hipStream_t stream);
 
 } // namespace qw
