@@ -167,7 +167,7 @@ int64_t route_blocks(int64_t tokens)
     return (tokens + per - 1) / per;
 }
 
-int64_t route_workspace(int64_t tokens, int64_t experts) { return route_blocks(tokens) * experts * 4; }
+int64_t route_workspace(int64_t tokens, int64_t experts) { return route_blocks(tokens) * ((experts + 3) / 4) * 16; }
 
 } // namespace
 
@@ -266,6 +266,7 @@ QW_API qw_status qw_route_experts(const void *logits, int dtype, int64_t tokens,
     a.counts = static_cast<int32_t *>(workspace);
     a.tokens_a_block = (int)qw::route_tokens_a_block(tokens);
     a.blocks = (int)route_blocks(tokens);
+    a.counts_stride = (int)((experts + 3) / 4 * 4);
     return status_of(qw::launch_route_experts(a, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -29,7 +29,8 @@ struct RouteArgs {
     int32_t *offsets;  // [experts + 1]
     int32_t *rows;     // [tokens * top_k]
     int32_t *places;   // [tokens][top_k]
-    int32_t *counts;   // workspace: [blocks][experts]
+    int32_t *counts;   // workspace: [blocks][counts_stride]
+    int counts_stride; // experts, up to a multiple of 4
     int tokens_a_block; // route_tokens_a_block()
     int blocks;         // that have tokens
 };
