@@ -885,27 +885,40 @@ QW_API qw_status qw_add_rms_norm_quantize(const void *x, int64_t x_stride, const
  *   residual    fp16 [m][columns of y], or null; may be y itself
  *   y           fp16 [m][n], gated [m][n / 2] (written)
  *
+ *   workspace   qw_w8a16_linear_workspace() bytes, or null
+ *
  * The kernels and their choice are qw_w8a16_gemm's, tuning records included.
+ * Where their grid would leave much of the chip idle, and there is a workspace,
+ * the reduction is split in parts whose sums are kept in it and added up, in
+ * order, by a second launch.
  * Accuracy: the sum as there, the activations within 2^-17 relative (of v for
  * the gelus' and silu's negative tails beyond -6).
- * qw_w8a16_linear_path forces a kernel, and for QW_PATH_MFMA with a nonzero
- * `tile` that tile (as qw_w8a16_gemm_tile).
+ * qw_w8a16_linear_path forces a kernel, for QW_PATH_MFMA with a nonzero `tile`
+ * that tile (as qw_w8a16_gemm_tile), and with tile 256256 the number of parts
+ * (`splits`, else 1; workspace: 262144 bytes for each part of each 256 x 256
+ * tile).
  *
  * Errors: as qw_w8a16_gemm_path, plus QW_ERROR_INVALID_VALUE for an unknown
  * activation, gated not 0 or 1 or with an odd n, an unknown tile or one without
- * QW_PATH_MFMA, or y overlapping bias, or residual at another place than its
- * own, and QW_ERROR_UNSUPPORTED where a forced kernel does not take the sizes:
- * QW_PATH_GEMV with m > 2, or gated with k > 8192, QW_PATH_MFMA gated with
- * n * k >= 2^32.
+ * QW_PATH_MFMA, splits below 1 or above 64 or without tile 256256, a workspace
+ * that is too small or overlaps anything, y overlapping bias, or residual at
+ * another place than its own, and QW_ERROR_UNSUPPORTED where a forced kernel
+ * does not take the sizes: QW_PATH_GEMV with m > 2, or gated with k > 8192,
+ * QW_PATH_MFMA gated with n * k >= 2^32, k < 64 * splits.
+ *
+ * qw_w8a16_linear_workspace -- workspace bytes for these sizes on the current
+ * device (0: none needed), -1 for sizes that the call rejects.
  */
 QW_API qw_status qw_w8a16_linear(const uint16_t *x, const int8_t *q, const uint16_t *scales,
                                  const uint16_t *bias, int activation, int gated,
                                  const uint16_t *residual, uint16_t *y, int64_t m, int64_t n,
-                                 int64_t k, void *stream);
+                                 int64_t k, void *workspace, int64_t workspace_bytes, void *stream);
 QW_API qw_status qw_w8a16_linear_path(const uint16_t *x, const int8_t *q, const uint16_t *scales,
                                       const uint16_t *bias, int activation, int gated,
                                       const uint16_t *residual, uint16_t *y, int64_t m, int64_t n,
-                                      int64_t k, int path, int tile, void *stream);
+                                      int64_t k, int path, int tile, int splits, void *workspace,
+                                      int64_t workspace_bytes, void *stream);
+QW_API int64_t qw_w8a16_linear_workspace(int64_t m, int64_t n, int64_t k, int gated);
 
 /*
  * qw_w8a8_linear -- the same for qw_w8a8_gemm's operands:
@@ -914,7 +927,7 @@ QW_API qw_status qw_w8a16_linear_path(const uint16_t *x, const int8_t *q, const 
  *
  *   qx, sx, q, scales, m, n, k, stream   as qw_w8a8_gemm
  *   dtype       of bias, residual and y (qw_dtype)
- *   others as qw_w8a16_linear
+ *   others as qw_w8a16_linear (qw_w8a8_linear_workspace)
  *
  * Errors: as qw_w8a8_gemm_path and qw_w8a16_linear_path, plus
  * QW_ERROR_INVALID_VALUE for an unknown dtype.
@@ -922,11 +935,13 @@ QW_API qw_status qw_w8a16_linear_path(const uint16_t *x, const int8_t *q, const 
 QW_API qw_status qw_w8a8_linear(const int8_t *qx, const uint16_t *sx, const int8_t *q,
                                 const uint16_t *scales, const void *bias, int activation, int gated,
                                 const void *residual, int dtype, void *y, int64_t m, int64_t n,
-                                int64_t k, void *stream);
+                                int64_t k, void *workspace, int64_t workspace_bytes, void *stream);
 QW_API qw_status qw_w8a8_linear_path(const int8_t *qx, const uint16_t *sx, const int8_t *q,
                                      const uint16_t *scales, const void *bias, int activation,
                                      int gated, const void *residual, int dtype, void *y, int64_t m,
-                                     int64_t n, int64_t k, int path, int tile, void *stream);
+                                     int64_t n, int64_t k, int path, int tile, int splits,
+                                     void *workspace, int64_t workspace_bytes, void *stream);
+QW_API int64_t qw_w8a8_linear_workspace(int64_t m, int64_t n, int64_t k, int gated);
 
 /* Most experts and most of them a token that qw_route_experts takes. */
 #define QW_MAX_EXPERTS 512

@@ -26,30 +26,74 @@ bool known_tile(int tile, bool a8)
     return tile == 256256 || tile == 256128 || tile == 256064 || (tile == 128128 && !a8) || tile == 128064;
 }
 
-// The kernel and tile of a linear call: a tuning record of the plain product's
-// bucket, else its rule, where the kernel takes the sizes.
-void choose(const qw::LinearArgs &a, int &path, int &tile)
+// Parts to split the reduction of a ping-pong grid into: as many as fill the
+// CUs, at most 8, where its tiles cover at most half of them and the reduction
+// is long.  The accumulators' way to memory and back, and the second launch,
+// cost some 30 to 50 us with all CUs at work.  Us, best tile without a split /
+// split, k = 8192, 11008, 13696, 20480, n = 4096: W8A8 256 rows 60 / 52, 77 / 58,
+// 93 / 61, 143 / 78; 512 rows 63 / 59, 80 / 66, 93 / 69, 146 / 86; 2048 rows 116 /
+// 98, 149 / 117, 176 / 134, 270 / 187; W8A16 512 rows 71 / 69, 111 / 79, 140 / 87,
+// 206 / 107; 2048 rows 142 / 141, 186 / 177, 229 / 211, 336 / 298.  With k = 4096
+// no part count gained: W8A8 512 rows 26 / 43, 2048 rows 55 / 66.
+int split_parts(int64_t m, int64_t n, int64_t k, bool gated)
 {
-    const bool a8 = a.sx != nullptr;
-    const int tuned = qw::tuned_choice(a.m, a.n, a.k, a8);
-    path = tuned >= 0 ? tuned / qw::kChoicePath : qw::auto_path(a.m, a.n, a.k);
-    tile = tuned >= 0 ? tuned % qw::kChoicePath : 0;
-    if (path == QW_PATH_GEMV && (a8 || !qw::gemv_linear_supported(a.m, a.k, a.gated)))
-        path = QW_PATH_SKINNY;
-    if (path == QW_PATH_SKINNY && a.m > 16 * 65535)
-        path = QW_PATH_MFMA;
-    if (path == QW_PATH_MFMA && !qw::mfma_linear_supported(a.n, a.k, a.gated))
-        path = QW_PATH_SKINNY;
-    if (path != QW_PATH_MFMA || (tile == 256256 && a.k > qw::kPingPongMaxK) || !known_tile(tile, a8))
-        tile = 0;
+    const int64_t columns = gated ? n / 2 : n, bn = gated ? 128 : 256;
+    const int64_t tiles = ((m + 255) / 256) * ((columns + bn - 1) / bn), cus = qw::device_cu_count();
+    if (k < 8192 || 2 * tiles > cus)
+        return 1;
+    return (int)(cus / tiles < 8 ? cus / tiles : 8);
 }
 
-qw_status linear(qw::LinearArgs a, int dtype, int gated, int path, int tile, void *stream)
+// The kernel, tile and parts of a linear call: a tuning record of the plain
+// product's bucket, else its rule, where the kernel takes the sizes; without a
+// record a split ping-pong grid where that gains.
+struct LinearPlan {
+    int path, tile, splits;
+};
+
+LinearPlan plan_linear(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
+{
+    const int tuned = qw::tuned_choice(m, n, k, a8);
+    LinearPlan p = {tuned >= 0 ? tuned / qw::kChoicePath : qw::auto_path(m, n, k), tuned >= 0 ? tuned % qw::kChoicePath : 0, 1};
+    if (p.path == QW_PATH_GEMV && (a8 || !qw::gemv_linear_supported(m, k, gated)))
+        p.path = QW_PATH_SKINNY;
+    if (p.path == QW_PATH_SKINNY && m > 16 * 65535)
+        p.path = QW_PATH_MFMA;
+    if (p.path == QW_PATH_MFMA && !qw::mfma_linear_supported(n, k, gated))
+        p.path = QW_PATH_SKINNY;
+    if (p.path != QW_PATH_MFMA || (p.tile == 256256 && k > qw::kPingPongMaxK) || !known_tile(p.tile, a8))
+        p.tile = 0;
+    // (rounding m up to 256 rows costs at most a tenth over 64, as for the
+    // ping-pong tile without a split)
+    const int64_t rows256 = (m + 255) / 256 * 256, rows64 = (m + 63) / 64 * 64;
+    if (p.path == QW_PATH_MFMA && p.tile == 0 && k <= qw::kPingPongMaxK && 10 * rows256 <= 11 * rows64) {
+        p.splits = split_parts(m, n, k, gated);
+        if (p.splits > 1)
+            p.tile = 256256;
+    }
+    return p;
+}
+
+int64_t linear_workspace(int64_t m, int64_t n, int64_t k, int gated, bool a8)
+{
+    if (m < 0 || n < 0 || k <= 0 || (gated != 0 && gated != 1) || (gated && n % 2) || k % 16 != 0 || m > kMaxDim || n > kMaxDim ||
+        k > (a8 ? (int64_t)QW_W8A8_MAX_K : kMaxDim))
+        return -1;
+    if (m == 0 || n == 0)
+        return 0;
+    const LinearPlan p = plan_linear(m, n, k, gated != 0, a8);
+    return p.splits > 1 ? qw::mfma_split_bytes(m, n, p.splits) : 0;
+}
+
+qw_status linear(qw::LinearArgs a, int dtype, int gated, LinearPlan p, void *workspace, int64_t workspace_bytes, void *stream)
 {
     const bool a8 = a.sx != nullptr;
-    if (path != QW_PATH_AUTO && path != QW_PATH_MFMA && path != QW_PATH_SKINNY && (a8 || path != QW_PATH_GEMV))
+    if (p.path != QW_PATH_AUTO && p.path != QW_PATH_MFMA && p.path != QW_PATH_SKINNY && (a8 || p.path != QW_PATH_GEMV))
         return QW_ERROR_INVALID_VALUE;
-    if (tile != 0 && (path != QW_PATH_MFMA || !known_tile(tile, a8)))
+    if (p.tile != 0 && (p.path != QW_PATH_MFMA || !known_tile(p.tile, a8)))
+        return QW_ERROR_INVALID_VALUE;
+    if (p.splits < 1 || p.splits > 64 || (p.splits > 1 && p.tile != 256256) || workspace_bytes < 0 ||
+        (workspace == nullptr && workspace_bytes > 0))
         return QW_ERROR_INVALID_VALUE;
     if (a.m < 0 || a.n < 0 || a.k <= 0 || (gated != 0 && gated != 1) || (gated && a.n % 2) ||
         a.ep.activation < QW_ACT_NONE || a.ep.activation > QW_ACT_SILU || (dtype != QW_F16 && dtype != QW_BF16))
@@ -70,25 +114,43 @@ qw_status linear(qw::LinearArgs a, int dtype, int gated, int path, int tile, voi
         meet(a.y, ybytes, a.scales, n * 2u) || meet(a.y, ybytes, a.ep.bias, n * 2u) ||
         (a.ep.residual != a.y && meet(a.y, ybytes, a.ep.residual, ybytes)))
         return QW_ERROR_INVALID_VALUE;
-    if (path == QW_PATH_AUTO)
-        choose(a, path, tile);
+    if (p.path == QW_PATH_AUTO) {
+        p = plan_linear(a.m, a.n, a.k, a.gated, a8);
+        if (p.splits > 1 && workspace == nullptr)
+            p.splits = 1, p.tile = 0; // (a caller may do without)
+    }
+    if (p.splits > 1) {
+        const int64_t need = qw::mfma_split_bytes(a.m, a.n, p.splits);
+        if (workspace == nullptr || workspace_bytes < need)
+            return QW_ERROR_INVALID_VALUE;
+        if (off16(workspace))
+            return QW_ERROR_MISALIGNED;
+        const void *used[7] = {a.x, a.sx, a.q, a.scales, a.ep.bias, a.ep.residual, a.y};
+        const uint64_t size[7] = {m * k * (a8 ? 1u : 2u), m * 2u, n * k, n * 2u, n * 2u, ybytes, ybytes};
+        for (int i = 0; i < 7; ++i)
+            if (meet(workspace, (uint64_t)need, used[i], size[i]))
+                return QW_ERROR_INVALID_VALUE;
+    }
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (path == QW_PATH_GEMV) {
+    if (p.path == QW_PATH_GEMV) {
         if (!qw::gemv_linear_supported(a.m, a.k, a.gated))
             return QW_ERROR_UNSUPPORTED;
         return status_of(qw::launch_gemv_linear(static_cast<const uint16_t *>(a.x), a.q, a.scales, a.ep, a.gated, a.y, a.m, a.n,
                                                 a.k, s));
     }
-    if (path == QW_PATH_SKINNY) {
+    if (p.path == QW_PATH_SKINNY) {
         if (a.m > 16 * 65535)
             return QW_ERROR_UNSUPPORTED;
         return status_of(qw::launch_skinny_linear(a, s));
     }
-    if (!qw::mfma_linear_supported(a.n, a.k, a.gated) || (tile == 256256 && a.k > qw::kPingPongMaxK))
+    if (!qw::mfma_linear_supported(a.n, a.k, a.gated) || (p.tile == 256256 && a.k > qw::kPingPongMaxK) ||
+        (p.splits > 1 && a.k < 64 * p.splits))
         return QW_ERROR_UNSUPPORTED;
-    if (tile == 0)
-        tile = a8 ? qw::w8a8_tile_choice(a.m, a.n, a.k) : qw::mfma_tile_choice(a.m, a.n, a.k);
-    return status_of(a8 ? qw::launch_mfma_linear_a8(tile, a, s) : qw::launch_mfma_linear(tile, a, s));
+    if (p.splits > 1)
+        return status_of(a8 ? qw::launch_mfma_split_a8(p.splits, a, workspace, s) : qw::launch_mfma_split(p.splits, a, workspace, s));
+    if (p.tile == 0)
+        p.tile = a8 ? qw::w8a8_tile_choice(a.m, a.n, a.k) : qw::mfma_tile_choice(a.m, a.n, a.k);
+    return status_of(a8 ? qw::launch_mfma_linear_a8(p.tile, a, s) : qw::launch_mfma_linear(p.tile, a, s));
 }
 
 struct Span {
@@ -343,24 +405,37 @@ QW_API qw_status qw_experts_combine(const uint16_t *y, int64_t entries, const in
     return status_of(qw::launch_experts_combine(a, static_cast<hipStream_t>(stream)));
 }
 
+QW_API int64_t qw_w8a16_linear_workspace(int64_t m, int64_t n, int64_t k, int gated)
+{
+    return linear_workspace(m, n, k, gated, false);
+}
+
+QW_API int64_t qw_w8a8_linear_workspace(int64_t m, int64_t n, int64_t k, int gated)
+{
+    return linear_workspace(m, n, k, gated, true);
+}
+
 QW_API qw_status qw_w8a16_linear_path(const uint16_t *x, const int8_t *q, const uint16_t *scales, const uint16_t *bias,
                                       int activation, int gated, const uint16_t *residual, uint16_t *y, int64_t m,
-                                      int64_t n, int64_t k, int path, int tile, void *stream)
+                                      int64_t n, int64_t k, int path, int tile, int splits, void *workspace,
+                                      int64_t workspace_bytes, void *stream)
 {
     const qw::LinearArgs a = {x, nullptr, q, scales, {bias, residual, activation, 0}, false, y, m, n, k};
-    return linear(a, QW_F16, gated, path, tile, stream);
+    return linear(a, QW_F16, gated, {path, tile, splits}, workspace, workspace_bytes, stream);
 }
 
 QW_API qw_status qw_w8a16_linear(const uint16_t *x, const int8_t *q, const uint16_t *scales, const uint16_t *bias,
                                  int activation, int gated, const uint16_t *residual, uint16_t *y, int64_t m, int64_t n,
-                                 int64_t k, void *stream)
+                                 int64_t k, void *workspace, int64_t workspace_bytes, void *stream)
 {
-    return qw_w8a16_linear_path(x, q, scales, bias, activation, gated, residual, y, m, n, k, QW_PATH_AUTO, 0, stream);
+    return qw_w8a16_linear_path(x, q, scales, bias, activation, gated, residual, y, m, n, k, QW_PATH_AUTO, 0, 1, workspace,
+                                workspace_bytes, stream);
 }
 
 QW_API qw_status qw_w8a8_linear_path(const int8_t *qx, const uint16_t *sx, const int8_t *q, const uint16_t *scales,
                                      const void *bias, int activation, int gated, const void *residual, int dtype, void *y,
-                                     int64_t m, int64_t n, int64_t k, int path, int tile, void *stream)
+                                     int64_t m, int64_t n, int64_t k, int path, int tile, int splits, void *workspace,
+                                     int64_t workspace_bytes, void *stream)
 {
     if (!sx && m != 0 && n != 0)
         return QW_ERROR_INVALID_VALUE;
@@ -369,15 +444,15 @@ QW_API qw_status qw_w8a8_linear_path(const int8_t *qx, const uint16_t *sx, const
     const qw::LinearArgs a = {qx, sx ? sx : &empty, q, scales,
                               {static_cast<const uint16_t *>(bias), static_cast<const uint16_t *>(residual), activation, 0},
                               false, static_cast<uint16_t *>(y), m, n, k};
-    return linear(a, dtype, gated, path, tile, stream);
+    return linear(a, dtype, gated, {path, tile, splits}, workspace, workspace_bytes, stream);
 }
 
 QW_API qw_status qw_w8a8_linear(const int8_t *qx, const uint16_t *sx, const int8_t *q, const uint16_t *scales,
                                 const void *bias, int activation, int gated, const void *residual, int dtype, void *y,
-                                int64_t m, int64_t n, int64_t k, void *stream)
+                                int64_t m, int64_t n, int64_t k, void *workspace, int64_t workspace_bytes, void *stream)
 {
-    return qw_w8a8_linear_path(qx, sx, q, scales, bias, activation, gated, residual, dtype, y, m, n, k, QW_PATH_AUTO, 0,
-                               stream);
+    return qw_w8a8_linear_path(qx, sx, q, scales, bias, activation, gated, residual, dtype, y, m, n, k, QW_PATH_AUTO, 0, 1,
+                               workspace, workspace_bytes, stream);
 }
 
 } // extern "C"

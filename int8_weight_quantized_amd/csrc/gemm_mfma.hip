@@ -175,7 +175,7 @@ hipError_t launch_pp(const void *x, const uint16_t *sx, const int8_t *q, const u
     const int group = pp_group_width<A8>(blocks, tiles_m, tiles_n);
 #define QW_PP_LAUNCH(A, O, Z)                                                                                   \
     hipLaunchKernelGGL((mfma_pp_kernel<A, O, Z>), dim3((unsigned)blocks), dim3(pp::kThreads), 0, stream, x, sx, q,  \
-                       scales, zeros, ol, y, (int)m, (int)n, (int)k, (int)tiles_m, (int)tiles_n, group, Epilogue{}, Experts{})
+                       scales, zeros, ol, y, (int)m, (int)n, (int)k, (int)tiles_m, (int)tiles_n, group, Epilogue{}, Experts{}, 1, nullptr)
     if constexpr (A8) {
         if (ol.idx != nullptr || zeros != nullptr)
             return hipErrorInvalidValue;

@@ -117,17 +117,20 @@ __device__ __forceinline__ int xcd_remap(int bid, int nblocks)
 // there by the lane that holds the output: one rounding.
 // ---------------------------------------------------------------------------
 
+constexpr bool is_gated(int epi) { return epi == kGated || epi == kPartialGated; }
+constexpr bool is_partial(int epi) { return epi == kPartial || epi == kPartialGated; }
+
 // Weight row of tile row r (or of the row clamped to the matrix): r itself, or
 // a channel of either half.  n_out: columns of Y, n0: the tile's first.
 template <int EPI>
 __device__ __forceinline__ int tile_channel(int r)
 {
-    return EPI == kGated ? (r >> 4) * 8 + (r & 7) : r;
+    return is_gated(EPI) ? (r >> 4) * 8 + (r & 7) : r;
 }
 template <int EPI>
 __device__ __forceinline__ int tile_half(int r)
 {
-    return EPI == kGated ? (r >> 3) & 1 : 0;
+    return is_gated(EPI) ? (r >> 3) & 1 : 0;
 }
 
 // put(i, j, qd, o) for every four outputs o = act(v), or their products with
@@ -911,7 +914,7 @@ struct Cfg {
     static constexpr int kImageRow[2] = {kBN * 2 + 16, kBN + 16};
     static constexpr int stage_alloc(int epi)
     {
-        const int image = epi == kPlain ? 0 : kImageRows * kImageRow[epi == kGated];
+        const int image = epi == kPlain || is_partial(epi) ? 0 : kImageRows * kImageRow[epi == kGated];
         return kStageAlloc > image ? kStageAlloc : image;
     }
     static_assert(3 * kImageRows >= kBM, "image split");
@@ -926,17 +929,21 @@ static_assert(pp::kBM * kPingPongMaxK * 2 <= (int64_t(1) << 31), "buffer range")
 // sx; the MFMA is v_mfma_i32_32x32x32_i8 (two per 64-wide k step and tile,
 // no casts), int32 accumulators, and the epilogue multiplies by S[n] * Sx[m].
 // Otherwise xv is fp16 and sx unused.
+// EPI kPartial, kPartialGated: the grid holds `splits` copies of the tiles, of which copy s
+// multiplies the k steps from s / splits of them on and leaves its accumulators
+// in `partial`, [copy][tile][quad of registers][thread], for mfma_join_kernel.
 template <bool A8, bool OL, bool ZP, int EPI = kPlain, bool GRP = false>
 __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
     const void *__restrict__ xv, const uint16_t *__restrict__ sx, const int8_t *__restrict__ q,
     const uint16_t *__restrict__ scales, const int8_t *__restrict__ zeros, OutlierList ol,
-    uint16_t *__restrict__ y, int m, int n, int k, int tiles_m, int tiles_n, int group, Epilogue ep, Experts ex)
+    uint16_t *__restrict__ y, int m, int n, int k, int tiles_m, int tiles_n, int group, Epilogue ep, Experts ex,
+    int splits, u32x4_t *__restrict__ partial)
 {
     static_assert(EPI == kPlain || (!OL && !ZP), "an epilogue goes with symmetric codes");
     static_assert(!GRP || (EPI != kPlain && !A8), "grouped products are W8A16 with an epilogue");
     using namespace pp;
-    constexpr int kCols = EPI == kGated ? kBN / 2 : kBN; // columns of Y a tile
-    const int n_out = EPI == kGated ? n / 2 : n;
+    constexpr int kCols = is_gated(EPI) ? kBN / 2 : kBN; // columns of Y a tile
+    const int n_out = is_gated(EPI) ? n / 2 : n;
     using C = Cfg<A8>;
     constexpr int kStage = C::kStage;
     constexpr int kWInstr = C::kWInstr;
@@ -968,7 +975,9 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
     const int grp = wave / 4;
     const int nw = wave % 4;
 
-    const int tile = xcd_remap(blockIdx.x, tiles_m * tiles_n);
+    const int block = xcd_remap(blockIdx.x, tiles_m * tiles_n * (is_partial(EPI) ? splits : 1));
+    const int split = is_partial(EPI) ? block / (tiles_m * tiles_n) : 0;
+    const int tile = is_partial(EPI) ? block - split * (tiles_m * tiles_n) : block;
     const int gsize = group * tiles_m;
     const int gi = tile / gsize;
     const int gl = tile - gi * gsize;
@@ -992,8 +1001,13 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
         if (ep.bias)
             ep.bias += (int64_t)rows.expert * n;
     }
-    const int ktiles = (k + kBK - 1) / kBK;
-    const int full_tiles = (k % kBK) != 0 ? ktiles - 1 : ktiles;
+    // this workgroup's part of the reduction: columns [kfirst, kfirst + klen)
+    const int all_ktiles = (k + kBK - 1) / kBK;
+    const int kfirst = is_partial(EPI) ? (int)((int64_t)all_ktiles * split / splits) * kBK : 0;
+    const int klen =
+        is_partial(EPI) ? min(k, (int)((int64_t)all_ktiles * (split + 1) / splits) * kBK) - kfirst : k;
+    const int ktiles = (klen + kBK - 1) / kBK;
+    const int full_tiles = (klen % kBK) != 0 ? ktiles - 1 : ktiles;
 
     // Copy sources: as in the 4-wave kernel, with 8 waves sharing a tile.
     // Copy i of a wave covers rows 16 i (weight) or 8 i (activations) below
@@ -1007,9 +1021,9 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
     constexpr int kXE = A8 ? 1 : 2; // bytes per activation element
     // (a gated product's tile row r is channel tile_channel(r) of half
     // tile_half(r), so a copy of 16 rows is 8 channels of both halves)
-    constexpr int kWStep = EPI == kGated ? 8 : 16; // channels a weight copy
+    constexpr int kWStep = is_gated(EPI) ? 8 : 16; // channels a weight copy
     const uint32_t woff =
-        EPI == kGated ? (uint32_t)(tile_half<EPI>(lane / 4) * n_out + wave * kWInstr * 8 + tile_channel<EPI>(lane / 4)) *
+        is_gated(EPI) ? (uint32_t)(tile_half<EPI>(lane / 4) * n_out + wave * kWInstr * 8 + tile_channel<EPI>(lane / 4)) *
                                 (uint32_t)k + wchunk * 16
                       : (uint32_t)((wave * kWInstr * 16 + lane / 4) * k + wchunk * 16);
     // A8: activation copy i covers rows 16 i below copy 0, like the weight
@@ -1028,16 +1042,16 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
     // (the scalar offset of activation copy i, written out at each use: as a
     // lambda or a template helper it kept the host pass from emitting the
     // kernels' launch stubs)
-    const int8_t *wtile = q + (int64_t)n0 * k;
-    const uint8_t *xtile = static_cast<const uint8_t *>(xv) + (GRP && ex.rows ? 0 : (int64_t)m0 * k * kXE);
+    const int8_t *wtile = q + (int64_t)n0 * k + kfirst;
+    const uint8_t *xtile = static_cast<const uint8_t *>(xv) + (GRP && ex.rows ? 0 : (int64_t)m0 * k * kXE) + kfirst * kXE;
     const __amdgpu_buffer_rsrc_t wrsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<int8_t *>(wtile), (short)0,
-        static_cast<int>(static_cast<uint32_t>((EPI == kGated ? (int64_t)(n - n0) : min((int64_t)kBN, (int64_t)(n - n0))) * k)),
+        static_cast<int>(static_cast<uint32_t>((is_gated(EPI) ? (int64_t)(n - n0) : min((int64_t)kBN, (int64_t)(n - n0))) * k - kfirst)),
         kBufferFlags);
     const __amdgpu_buffer_rsrc_t xrsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t *>(xtile), (short)0,
         static_cast<int>(static_cast<uint32_t>(
-            (GRP && ex.rows ? (int64_t)ex.x_rows : min((int64_t)kBM, (int64_t)(m - m0))) * k * kXE)),
+            (GRP && ex.rows ? (int64_t)ex.x_rows : min((int64_t)kBM, (int64_t)(m - m0))) * k * kXE - kfirst * kXE)),
         kBufferFlags);
 
     // this wave's share of the copies of tile kt into stage array st
@@ -1067,7 +1081,7 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
         for (int i = 0; i < kXInstr; ++i) {
             uint8_t *dst = st + kWBytes + (wave * kXInstr + i) * 1024;
             const int gk = k0 + (A8 ? wchunk * 16 : ((i & 1) ? xchunk_odd : xchunk_even) * 8);
-            if (gk < k)
+            if (gk < klen)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     xrsrc, (lds_ptr_t)dst, 16, GRP ? (int)xoff[GRP ? i : 0] : (int)((i & 1) ? xoff_odd : xoff_even),
                     GRP ? k0 * 2 : (A8 ? k0 + i * 16 * k : (k0 + (i & ~1) * 8 * k) * 2), 0, 0);
@@ -1231,7 +1245,7 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
     issue(0, ring0, partial_t{});
     issue(1, ring1, partial_t{});
     for (int c = tid; c < kBN; c += kThreads) {
-        if constexpr (EPI == kPlain) {
+        if constexpr (EPI == kPlain || is_partial(EPI)) {
             scale_lds[c] = n0 + c < n ? f16_bits_to_f32(scales[n0 + c]) : 0.0f;
         } else {
             const int col = n0 + tile_channel<EPI>(c), row = tile_half<EPI>(c) * n_out + col;
@@ -1297,10 +1311,28 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
     }
 
     // ---- epilogue: one group at a time through an LDS image of its rows ----
+    if constexpr (is_partial(EPI)) {
+        u32x4_t *dst = partial + (int64_t)block * (kSI * kSJ * 4) * kThreads + tid;
+#pragma unroll
+        for (int i = 0; i < kSI; ++i)
+#pragma unroll
+            for (int j = 0; j < kSJ; ++j)
+#pragma unroll
+                for (int qd = 0; qd < 4; ++qd) {
+                    u32x4_t v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const auto a = acc[i][j][4 * qd + e];
+                        v[e] = __builtin_bit_cast(uint32_t, a);
+                    }
+                    dst[((i * kSJ + j) * 4 + qd) * kThreads] = v;
+                }
+        return;
+    }
     if constexpr (EPI != kPlain) {
         // One image of all 256 rows over the three stages, which are free from
         // phase 2T on: group 0 fills its half while group 1 finishes its MFMAs.
-        constexpr int kRow = C::kImageRow[EPI == kGated]; // image row
+        constexpr int kRow = C::kImageRow[is_gated(EPI)]; // image row
         constexpr int kPieces = kCols / 8;
         const int rows = min(kBM, m - m0);
         const bool whole = (n_out % 8) == 0 && n0 + kCols <= n_out;
@@ -1453,6 +1485,87 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
         write_image();
     ring_barrier();
     store_rows(1);
+}
+
+// The sum of the split products' accumulators, copy by copy, and the epilogue:
+// a workgroup for each of a tile's two wave groups (128 rows), whose threads
+// take the registers that the threads of the same place left.
+template <bool A8, int EPI>
+__global__ __launch_bounds__(pp::kThreads / 2) void mfma_join_kernel(const u32x4_t *__restrict__ partial, int splits,
+                                                                     const uint16_t *__restrict__ sx,
+                                                                     const uint16_t *__restrict__ scales, uint16_t *__restrict__ y,
+                                                                     int m, int n, int tiles_m, int tiles_n, int group, Epilogue ep)
+{
+    static_assert(EPI == kLinear || EPI == kGated, "an epilogue");
+    using namespace pp;
+    constexpr int kHalf = kThreads / 2;
+    constexpr int kCols = EPI == kGated ? kBN / 2 : kBN; // columns of Y a tile
+    constexpr int kRow = kCols * 2 + 16, kPieces = kCols / 8;
+    const int n_out = EPI == kGated ? n / 2 : n;
+    __shared__ __attribute__((aligned(16))) uint8_t image[kGroupRows * kRow];
+    __shared__ __attribute__((aligned(16))) float scale_lds[kBN];
+    __shared__ __attribute__((aligned(16))) float bias_lds[kBN];
+    __shared__ __attribute__((aligned(16))) float xscale_lds[A8 ? kGroupRows : 1];
+    const int tid = threadIdx.x, lane = __lane_id(), nw = tid / kWave, lrow = lane % 32, lgrp = lane / 32;
+    const int tiles = tiles_m * tiles_n, tile = blockIdx.x / 2, grp = blockIdx.x % 2;
+    const int gsize = group * tiles_m, gi = tile / gsize, gl = tile - gi * gsize, gw = min(group, tiles_n - gi * group);
+    const int n0 = (gi * group + gl % gw) * kCols, m0 = gl / gw * kBM + grp * kGroupRows;
+    const int rows = min(kGroupRows, m - m0);
+    if (rows <= 0)
+        return;
+    using acc_t = std::conditional_t<A8, int, float>;
+    acc_t acc[kSI][kSJ][16];
+    const u32x4_t *src = partial + (int64_t)tile * (kSI * kSJ * 4) * kThreads + grp * kHalf + tid;
+    auto add = [&](int s, auto first) {
+#pragma unroll
+        for (int i = 0; i < kSI; ++i)
+#pragma unroll
+            for (int j = 0; j < kSJ; ++j)
+#pragma unroll
+                for (int qd = 0; qd < 4; ++qd) {
+                    const u32x4_t v = __builtin_nontemporal_load(
+                        src + ((int64_t)s * tiles * (kSI * kSJ * 4) + (i * kSJ + j) * 4 + qd) * kThreads);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t b = v[e];
+                        const acc_t a = __builtin_bit_cast(acc_t, b);
+                        acc[i][j][4 * qd + e] = decltype(first)::value ? a : acc[i][j][4 * qd + e] + a;
+                    }
+                }
+    };
+    add(0, std::true_type{});
+    for (int s = 1; s < splits; ++s)
+        add(s, std::false_type{});
+    for (int c = tid; c < kBN; c += kHalf) {
+        const int col = n0 + tile_channel<EPI>(c), row = tile_half<EPI>(c) * n_out + col;
+        scale_lds[c] = col < n_out ? f16_bits_to_f32(scales[row]) : 0.0f;
+        bias_lds[c] = col < n_out && ep.bias ? from16(ep.bias[row], ep.bf16) : 0.0f;
+    }
+    if constexpr (A8)
+        for (int r = tid; r < kGroupRows; r += kHalf)
+            xscale_lds[r] = r < rows ? f16_bits_to_f32(sx[m0 + r]) : 0.0f;
+    const bool whole = (n_out % 8) == 0 && n0 + kCols <= n_out;
+    if (ep.residual)
+        for (int c = tid; c < rows * kPieces; c += kHalf)
+            *reinterpret_cast<u32x4_t *>(image + c / kPieces * kRow + c % kPieces * 16) =
+                load_row8(ep.residual + (int64_t)(m0 + c / kPieces) * n_out, n0 + c % kPieces * 8, n_out, whole);
+    __syncthreads();
+    activate_tile<EPI, kSI, kSJ>(
+        ep.activation,
+        [&](int i, int j, int qd, int e) -> float {
+            const int nl = nw * (kSI * 32) + i * 32 + 8 * qd + 4 * lgrp + e;
+            if constexpr (A8)
+                return fmaf((float)acc[i][j][4 * qd + e], scale_lds[nl] * xscale_lds[j * 32 + lrow], bias_lds[nl]);
+            else
+                return fmaf(acc[i][j][4 * qd + e], scale_lds[nl], bias_lds[nl]);
+        },
+        [&](int i, int j, int qd, float (&o)[4]) {
+            put4(image + (j * 32 + lrow) * kRow + tile_channel<EPI>(nw * (kSI * 32) + i * 32 + 8 * qd + 4 * lgrp) * 2, o, ep);
+        });
+    __syncthreads();
+    for (int c = tid; c < rows * kPieces; c += kHalf)
+        store_row8(y + (int64_t)(m0 + c / kPieces) * n_out, n0 + c % kPieces * 8, n_out, whole,
+                   *reinterpret_cast<const u32x4_t *>(image + c / kPieces * kRow + c % kPieces * 16));
 }
 
 } // namespace

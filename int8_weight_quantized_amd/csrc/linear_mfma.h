@@ -22,15 +22,15 @@ hipError_t launch_linear_tile(int tile, const LinearArgs &a, const Experts &ex, 
         return hipErrorInvalidConfiguration;
     const int group = GRP ? (int)tiles_n : mfma_tile_group(tile, A8, tiles_m, tiles_n);
     const OutlierList none = {nullptr, nullptr, 0};
-    auto launch = [&](auto kernel, int threads) {
+    auto launch = [&](auto kernel, int threads, auto... more) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, stream, a.x, a.sx, a.q, a.scales,
                            (const int8_t *)nullptr, none, a.y, (int)a.m, (int)a.n, (int)a.k, (int)tiles_m, (int)tiles_n,
-                           group, a.ep, ex);
+                           group, a.ep, ex, more...);
         return hipGetLastError();
     };
     if constexpr (kPp)
-        return a.gated ? launch(mfma_pp_kernel<A8, false, false, kGated, GRP>, pp::kThreads)
-                       : launch(mfma_pp_kernel<A8, false, false, kLinear, GRP>, pp::kThreads);
+        return a.gated ? launch(mfma_pp_kernel<A8, false, false, kGated, GRP>, pp::kThreads, 1, (u32x4_t *)nullptr)
+                       : launch(mfma_pp_kernel<A8, false, false, kLinear, GRP>, pp::kThreads, 1, (u32x4_t *)nullptr);
     else
         return a.gated ? launch(mfma_gemm_dma_kernel<NW, BN, BM, A8, false, false, kGated, GRP>, NW * kWave)
                        : launch(mfma_gemm_dma_kernel<NW, BN, BM, A8, false, false, kLinear, GRP>, NW * kWave);
@@ -55,6 +55,35 @@ hipError_t launch_linear_tiles(int tile, const LinearArgs &a, const Experts &ex,
     default:
         return hipErrorInvalidValue;
     }
+}
+
+// Two launches: the parts of the products, and their sum with the epilogue.
+template <bool A8>
+hipError_t launch_split(int splits, const LinearArgs &a, void *workspace, hipStream_t stream)
+{
+    const int64_t columns = a.gated ? a.n / 2 : a.n, bn = a.gated ? pp::kBN / 2 : pp::kBN;
+    const int64_t tiles_n = (columns + bn - 1) / bn, tiles_m = (a.m + pp::kBM - 1) / pp::kBM, tiles = tiles_m * tiles_n;
+    if (tiles * splits > 0x7fffffff || tiles > 0x3fffffff)
+        return hipErrorInvalidConfiguration;
+    const int group = mfma_tile_group(256256, A8, tiles_m, tiles_n);
+    u32x4_t *partial = static_cast<u32x4_t *>(workspace);
+    const OutlierList none = {nullptr, nullptr, 0};
+    auto product = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * splits)), dim3(pp::kThreads), 0, stream, a.x, a.sx, a.q, a.scales,
+                           (const int8_t *)nullptr, none, a.y, (int)a.m, (int)a.n, (int)a.k, (int)tiles_m, (int)tiles_n, group,
+                           a.ep, Experts{}, splits, partial);
+        return hipGetLastError();
+    };
+    const hipError_t e = a.gated ? product(mfma_pp_kernel<A8, false, false, kPartialGated>)
+                                 : product(mfma_pp_kernel<A8, false, false, kPartial>);
+    if (e != hipSuccess)
+        return e;
+    auto join = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(2 * tiles)), dim3(pp::kThreads / 2), 0, stream, (const u32x4_t *)partial,
+                           splits, a.sx, a.scales, a.y, (int)a.m, (int)a.n, (int)tiles_m, (int)tiles_n, group, a.ep);
+        return hipGetLastError();
+    };
+    return a.gated ? join(mfma_join_kernel<A8, kGated>) : join(mfma_join_kernel<A8, kLinear>);
 }
 
 } // namespace

@@ -41,7 +41,7 @@ struct Epilogue {
     int activation;           // QW_ACT_*
     int bf16;
 };
-enum { kPlain = 0, kLinear = 1, kGated = 2 };
+enum { kPlain = 0, kLinear = 1, kGated = 2, kPartial = 3, kPartialGated = 4 };
 
 // A grouped product (GRP of the kernels): entry p of `entries` belongs to the
 // expert e with offsets[e] <= p < offsets[e + 1], whose weight is the e-th of
@@ -186,6 +186,11 @@ hipError_t launch_skinny_linear(const LinearArgs &a, hipStream_t stream);
 bool mfma_linear_supported(int64_t n, int64_t k, bool gated);
 hipError_t launch_mfma_linear(int tile, const LinearArgs &a, hipStream_t stream);
 hipError_t launch_mfma_linear_a8(int tile, const LinearArgs &a, hipStream_t stream);
+// The ping-pong tile with its reduction in `splits` parts, whose accumulators
+// take mfma_split_bytes() of workspace.
+int64_t mfma_split_bytes(int64_t m, int64_t n, int splits);
+hipError_t launch_mfma_split(int splits, const LinearArgs &a, void *workspace, hipStream_t stream);
+hipError_t launch_mfma_split_a8(int splits, const LinearArgs &a, void *workspace, hipStream_t stream);
 // Grouped: a.m entries.
 hipError_t launch_skinny_experts(const LinearArgs &a, const Experts &ex, hipStream_t stream);
 hipError_t launch_mfma_experts(int tile, const LinearArgs &a, const Experts &ex, hipStream_t stream);

@@ -47,10 +47,15 @@ def _declare(lib):
     norm = [vp, i64, vp, i64, vp, i32, i64, i64, f64, vp, i64]
     lib.qw_add_rms_norm.argtypes = norm + [vp, vp]
     lib.qw_add_rms_norm_quantize.argtypes = norm + [vp, vp, vp]
-    lib.qw_w8a16_linear.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i64, i64, i64, vp]
-    lib.qw_w8a16_linear_path.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i64, i64, i64, i32, i32, vp]
-    lib.qw_w8a8_linear.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i32, vp, i64, i64, i64, vp]
-    lib.qw_w8a8_linear_path.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i32, vp, i64, i64, i64, i32, i32, vp]
+    linear = [vp, vp, vp, vp, i32, i32, vp, vp, i64, i64, i64]
+    lib.qw_w8a16_linear.argtypes = linear + [vp, i64, vp]
+    lib.qw_w8a16_linear_path.argtypes = linear + [i32, i32, i32, vp, i64, vp]
+    linear = [vp, vp, vp, vp, vp, i32, i32, vp, i32, vp, i64, i64, i64]
+    lib.qw_w8a8_linear.argtypes = linear + [vp, i64, vp]
+    lib.qw_w8a8_linear_path.argtypes = linear + [i32, i32, i32, vp, i64, vp]
+    for f in (lib.qw_w8a16_linear_workspace, lib.qw_w8a8_linear_workspace):
+        f.argtypes = [i64, i64, i64, i32]
+        f.restype = i64
     lib.qw_route_experts.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, i64, i32, f64, vp, vp, vp, vp, vp, vp, i64, vp]
     lib.qw_route_experts_workspace.argtypes = [i64, i64, i64]
     experts = [vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, i64, i64, vp, i64, i64, i64]
@@ -197,6 +202,15 @@ def _activation(name):
         raise ValueError("activation must be one of %s, got %r" % (sorted(a for a in ACTIVATIONS if a), name)) from None
 
 
+def _workspace(need, device):
+    """Scratch memory of a product whose reduction is split: (tensor or None,
+    its address, its bytes).  Most take none."""
+    if need <= 0:
+        return None, None, 0
+    t = _kv._torch.empty(need, dtype=_kv._torch.uint8, device=device)
+    return t, t.data_ptr(), need
+
+
 def _validate_linear(x, q, scales, bias, gated, residual, out, dtype, device, sx=None):
     import torch
     check = _pkg._check
@@ -251,9 +265,11 @@ def w8a16_linear(x, q, scales, bias=None, activation=None, gated: bool = False, 
         index = x.get_device()
     if index != _kv._current_device():
         return _pkg._on_device(index, w8a16_linear, x, q, scales, bias, activation, gated, residual, out)
-    status = _pkg.library().qw_w8a16_linear(
+    lib = _pkg.library()
+    _held, ws, size = _workspace(lib.qw_w8a16_linear_workspace(m, n, k, 1 if gated else 0) if m > 16 else 0, x.device)
+    status = lib.qw_w8a16_linear(
         x.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(bias), act, 1 if gated else 0, _ptr(residual), y.data_ptr(), m, n, k,
-        _kv._raw_stream(index))
+        ws, size, _kv._raw_stream(index))
     if status:
         _raise(status, "qw_w8a16_linear")
     return y
@@ -292,9 +308,11 @@ def w8a8_linear(qx, sx, q, scales, bias=None, activation=None, gated: bool = Fal
         index = qx.get_device()
     if index != _kv._current_device():
         return _pkg._on_device(index, w8a8_linear, qx, sx, q, scales, bias, activation, gated, residual, dtype, out)
-    status = _pkg.library().qw_w8a8_linear(
+    lib = _pkg.library()
+    _held, ws, size = _workspace(lib.qw_w8a8_linear_workspace(m, n, k, 1 if gated else 0) if m > 16 else 0, qx.device)
+    status = lib.qw_w8a8_linear(
         qx.data_ptr(), sx.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(bias), act, 1 if gated else 0, _ptr(residual), code,
-        y.data_ptr(), m, n, k, _kv._raw_stream(index))
+        y.data_ptr(), m, n, k, ws, size, _kv._raw_stream(index))
     if status:
         _raise(status, "qw_w8a8_linear")
     return y

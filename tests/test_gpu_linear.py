@@ -28,28 +28,31 @@ def operands(seed, m, n, k, a8=False, dtype=F16, bias=True, residual=True, gated
     return x, sx, q, s, b, r
 
 
-def call(x, sx, q, s, b, r, act=None, gated=False, dtype=F16, path="auto", tile=0, out=None):
-    print("linear", tuple(x.shape), tuple(q.shape), "w8a8" if sx is not None else "w8a16", act, gated, dtype, path, tile, flush=True)
+def call(x, sx, q, s, b, r, act=None, gated=False, dtype=F16, path="auto", tile=0, out=None, splits=1):
+    print("linear", tuple(x.shape), tuple(q.shape), "w8a8" if sx is not None else "w8a16", act, gated, dtype, path, tile, splits, flush=True)
     (m, k), n = x.shape, q.shape[0]
     y = torch.full((m, n // 2 if gated else n), 77.0, dtype=dtype, device="cuda") if out is None else out
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     stream = torch.cuda.current_stream().cuda_stream
     lib = qw.library()
+    size = -(-m // 256) * -(-n // 256) * 262144 * splits if splits > 1 else 0
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda") if size else None
     if sx is None:
         st = lib.qw_w8a16_linear_path(p(x), p(q), p(s), p(b), qw.ACTIVATIONS[act], int(gated), p(r), p(y), m, n, k, PATHS[path],
-                                      tile, stream)
+                                      tile, splits, p(ws), size, stream)
     else:
         st = lib.qw_w8a8_linear_path(p(x), p(sx), p(q), p(s), p(b), qw.ACTIVATIONS[act], int(gated), p(r),
-                                     1 if dtype == BF16 else 0, p(y), m, n, k, PATHS[path], tile, stream)
+                                     1 if dtype == BF16 else 0, p(y), m, n, k, PATHS[path], tile, splits, p(ws), size, stream)
     assert st == 0, qw.status_string(st)
     return y
 
 
-def check(seed, m, n, k, a8=False, dtype=F16, act=None, gated=False, bias=True, residual=True, path="auto", tile=0):
+def check(seed, m, n, k, a8=False, dtype=F16, act=None, gated=False, bias=True, residual=True, path="auto", tile=0,
+          splits=1):
     ops = operands(seed, m, n, k, a8, dtype, bias, residual, gated)
     x, sx, q, s, b, r = ops
     want, off = linear64(x, q, s, b, act, gated, r, sx)
-    assert_rounded(call(*ops, act, gated, dtype, path, tile), want, off)
+    assert_rounded(call(*ops, act, gated, dtype, path, tile, splits=splits), want, off)
 
 
 @pytest.mark.parametrize("act", [None, "relu", "gelu", "gelu_tanh", "silu"])
@@ -105,6 +108,27 @@ def test_tiles(m, n, k, tile, gated):
 def test_tiles_w8a8(m, n, k, tile, gated):
     check(10, m, n, k, a8=True, act="silu" if gated else None, gated=gated, path="mfma", tile=tile)
     check(11, m, n, k, a8=True, dtype=BF16, gated=gated, path="mfma", tile=tile, bias=False)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("a8", [False, True])
+@pytest.mark.parametrize("m,n,k,splits", [(1, 2, 128, 2), (300, 518, 208, 3), (257, 264, 400, 2), (512, 1024, 1088, 8), (130, 1026, 4112, 5),
+                                          (256, 256, 640, 10), (700, 300, 2000, 7)])
+def test_split(m, n, k, splits, a8, gated):
+    check(24, m, n, k, a8=a8, act="silu" if gated else "gelu", gated=gated, path="mfma", tile=256256, splits=splits)
+    check(25, m, n, k, a8=a8, dtype=BF16 if a8 else F16, bias=False, residual=splits % 2 == 0, gated=gated, path="mfma", tile=256256,
+          splits=splits)
+
+
+@pytest.mark.parametrize("m,n,k", [(512, 1024, 8192), (250, 520, 13696), (700, 2048, 9232)])
+def test_split_by_itself(m, n, k):
+    """Sizes that the calls split on their own."""
+    x, _, q, s, b, r = operands(26, m, n, k)
+    want, off = linear64(x, q, s, b, "silu", False, r)
+    assert_rounded(qw.w8a16_linear(x, q, s, bias=b, activation="silu", residual=r), want, off)
+    x, sx, q, s, b, r = operands(27, m, n, k, a8=True, dtype=BF16, gated=True)
+    want, off = linear64(x, q, s, b, "silu", True, r, sx)
+    assert_rounded(qw.w8a8_linear(x, sx, q, s, bias=b, activation="silu", gated=True, residual=r), want, off)
 
 
 @pytest.mark.parametrize("tile", TILES)
