@@ -1018,8 +1018,9 @@ QW_API int64_t qw_route_experts_workspace(int64_t tokens, int64_t experts, int64
  *            is not one of x counts as a row of zeros
  *   y        fp16 [entries][n], gated [entries][n / 2] (written)
  *
- * Kernels: the skinny GEMM for up to 16 entries an expert on average, else the
- * MFMA GEMM; qw_w8a16_experts_path forces either, and a tile.  Accuracy as
+ * Kernels: the skinny GEMM for up to 12 entries an expert on average, else the
+ * MFMA GEMM, its tile picked by that average; qw_w8a16_experts_path forces
+ * either, and a tile (256256, 256128, 256064 or 128064).  Accuracy as
  * qw_w8a16_linear.
  *
  * Errors: as qw_w8a16_linear_path (which has QW_PATH_SKINNY and QW_PATH_MFMA

@@ -153,6 +153,21 @@ qw_status linear(qw::LinearArgs a, int dtype, int gated, LinearPlan p, void *wor
     return status_of(a8 ? qw::launch_mfma_linear_a8(p.tile, a, s) : qw::launch_mfma_linear(p.tile, a, s));
 }
 
+// The tile for a mean number of entries an expert.  A tile's rows belong to one
+// expert, so half a tile of each is in vain on average.  Us, 64 experts of 2048
+// (gated) by 2048, mean 16 / 64 / 128 / 384: 128 x 64 72 / 86 / 125 / 280, 256 x
+// 64 72 / 89 / 116 / 258, 256 x 128 98 / 108 / 125 / 248, 256 x 256 144 / 148 /
+// 156 / 272; 128 of 1536 by 2048, mean 16 / 32 / 128 / 256: 91 / 94 / 179 / 291,
+// 100 / 104 / 172 / 272, 119 / 119 / 179 / 259; 8 of 8192 by 4096, mean 512 / 2048:
+// 256 x 128 350 / 1076, 256 x 256 384 / 1046.  Up to 12 entries the skinny kernel:
+// mean 4 / 8 / 12 / 16 of the first 44 / 55 / 65 / 77.
+int experts_tile(int64_t mean, int64_t k)
+{
+    if (mean >= 1536 && k <= qw::kPingPongMaxK)
+        return 256256;
+    return mean >= 192 ? 256128 : mean >= 96 ? 256064 : 128064;
+}
+
 struct Span {
     const void *p;
     uint64_t n;
@@ -338,7 +353,7 @@ QW_API qw_status qw_w8a16_experts_path(const uint16_t *x, int64_t x_rows, int ga
                                        int64_t n, int64_t k, int path, int tile, void *stream)
 {
     if ((path != QW_PATH_AUTO && path != QW_PATH_SKINNY && path != QW_PATH_MFMA) ||
-        (tile != 0 && (path != QW_PATH_MFMA || !known_tile(tile, false))))
+        (tile != 0 && (path != QW_PATH_MFMA || !known_tile(tile, false) || tile == 128128)))
         return QW_ERROR_INVALID_VALUE;
     if (x_rows < 0 || entries < 0 || n < 0 || k <= 0 || experts < 1 || top_k < 1 || (gather != 0 && gather != 1) ||
         (!gather && x_rows != entries) || (gated != 0 && gated != 1) || (gated && n % 2) || activation < QW_ACT_NONE ||
@@ -363,13 +378,11 @@ QW_API qw_status qw_w8a16_experts_path(const uint16_t *x, int64_t x_rows, int ga
     const qw::Experts ex = {offsets, gather ? rows : nullptr, (int)experts, (int)entries, (int)x_rows, (int)top_k};
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (path == QW_PATH_AUTO)
-        path = entries <= 16 * experts && entries <= (1 << 19) ? QW_PATH_SKINNY : QW_PATH_MFMA;
+        path = entries <= 12 * experts && entries <= (1 << 19) ? QW_PATH_SKINNY : QW_PATH_MFMA;
     if (path == QW_PATH_SKINNY)
         return status_of(qw::launch_skinny_experts(a, ex, s));
-    if (tile == 0) {
-        const int64_t mean = entries / experts;
-        tile = mean >= 192 && k <= qw::kPingPongMaxK ? 256256 : mean >= 96 ? 256128 : mean >= 48 ? 256064 : 128064;
-    }
+    if (tile == 0)
+        tile = experts_tile(entries / experts, k);
     return status_of(qw::launch_mfma_experts(tile, a, ex, s));
 }
 

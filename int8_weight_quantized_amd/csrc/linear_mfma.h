@@ -47,7 +47,7 @@ hipError_t launch_linear_tiles(int tile, const LinearArgs &a, const Experts &ex,
     case 256064:
         return launch_linear_tile<4, 256, 64, A8, GRP>(tile, a, ex, stream);
     case 128128:
-        if constexpr (!A8)
+        if constexpr (!A8 && !GRP)
             return launch_linear_tile<4, 128, 128, A8, GRP>(tile, a, ex, stream);
         return hipErrorInvalidValue;
     case 128064:
