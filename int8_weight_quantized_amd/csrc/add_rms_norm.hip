@@ -12,6 +12,14 @@
 //
 // Bound by HBM: 7 bytes an element with a residual and codes.  A row is held in
 // registers, 8 elements (16 bytes) a lane and vector, as the 16-bit h.
+//
+// Waves before vectors: a row's latency is that of its loads and of the one
+// barrier, and a lane with one vector has the fewest of them in a row.  Us, fp16
+// with a residual / and codes, as launched and with four waves of four vectors:
+// 1 x 4096 2.5 / 2.7 and 3.1 / 3.4, 256 x 8192 4.2 / 4.6 and 5.0 / 5.4, 8192 x
+// 4096 38.9 / 35.0 and 40.2 / 38.8, 8192 x 8192 91 / 83 (5.9 and 5.6 TB/s) and
+// 95 / 89.  4096 x 16384 with two vectors 97 / 87, with eight 104 / 109.  2048 x
+// 65536 207 / 204.
 #include "ff_internal.h"
 #include "kv_device.h"
 
@@ -21,15 +29,13 @@ namespace {
 
 // W waves a row, at most V vectors a lane.
 template <int DT, bool CODES, int W, int V>
-__global__ __launch_bounds__(W == 1 ? 256 : W * kWave) void add_rms_norm_kernel(AddNormArgs a)
+__global__ __launch_bounds__(W * kWave) void add_rms_norm_kernel(AddNormArgs a)
 {
-    __shared__ float part[W > 1 ? 2 * W : 1];
+    __shared__ float part[2 * W];
     const int lane = __lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
-    if (row >= a.tokens)
-        return; // (whole waves, and only without a barrier below)
-    const int first = W == 1 ? lane : (int)threadIdx.x; // vector of the row
+    const int64_t row = blockIdx.x;
+    const int first = (int)threadIdx.x; // vector of the row
     const int vectors = (int)(a.k / 8);
     const uint16_t *x = a.x + row * a.x_stride, *r = a.residual + row * a.residual_stride;
     uint16_t *hrow = a.h + row * a.h_stride;
@@ -75,18 +81,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * kWave) void add_rms_norm_kernel(
         if (CODES)
             most = fmaxf(most, shfl_xor_f32(most, d));
     }
-    if constexpr (W > 1) {
-        if (lane == 0) {
-            part[wave] = squares;
-            part[W + wave] = most;
-        }
-        __syncthreads();
-        squares = 0.0f;
+    if (lane == 0) {
+        part[wave] = squares;
+        part[W + wave] = most;
+    }
+    __syncthreads();
+    squares = 0.0f;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            squares += part[i];
-            most = fmaxf(most, part[W + i]);
-        }
+    for (int i = 0; i < W; ++i) {
+        squares += part[i];
+        most = fmaxf(most, part[W + i]);
     }
     const float inv = 1.0f / sqrtf(squares / (float)a.k + a.eps);
     float step = 0.0f; // codes a unit of h w
@@ -125,8 +129,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * kWave) void add_rms_norm_kernel(
 template <int DT, bool CODES, int W, int V>
 hipError_t launch(const AddNormArgs &a, hipStream_t stream)
 {
-    const int64_t blocks = W == 1 ? (a.tokens + 3) / 4 : a.tokens;
-    add_rms_norm_kernel<DT, CODES, W, V><<<dim3((unsigned)blocks), dim3(W == 1 ? 256 : W * kWave), 0, stream>>>(a);
+    add_rms_norm_kernel<DT, CODES, W, V><<<dim3((unsigned)a.tokens), dim3(W * kWave), 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -136,8 +139,12 @@ hipError_t launch_sizes(const AddNormArgs &a, hipStream_t stream)
     const int64_t vectors = a.k / 8;
     if (vectors <= 256)
         return launch<DT, CODES, 4, 1>(a, stream);
+    if (vectors <= 512)
+        return launch<DT, CODES, 8, 1>(a, stream);
     if (vectors <= 1024)
-        return launch<DT, CODES, 4, 4>(a, stream);
+        return launch<DT, CODES, 16, 1>(a, stream);
+    if (vectors <= 2048)
+        return launch<DT, CODES, 16, 2>(a, stream);
     return launch<DT, CODES, 16, 8>(a, stream);
 }
 

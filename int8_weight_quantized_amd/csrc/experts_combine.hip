@@ -4,7 +4,9 @@
 //
 // in fp32, in the order of j, rounded once.  Bound by memory: top_k rows in, one
 // out (and the residual in).  A lane takes 8 columns (16 bytes) of a token and
-// asks for kBatch rows at a time, so that their latencies overlap.
+// asks for kBatch rows at a time, so that their latencies overlap.  4096 tokens of
+// 2048, 8 experts: 23 us (6.4 TB/s), with a residual 26; 16 tokens 3.4 us; 4096 of
+// 2047, by elements, 82.
 #include "ff_internal.h"
 #include "kv_device.h"
 
