@@ -393,11 +393,17 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, group
     return ExpertRoute(ids.view(tokens, top_k), weights, offsets, rows, places.view(tokens, top_k))
 
 
+def _check_route(route):
+    if not isinstance(route, ExpertRoute):
+        raise TypeError("route must be an ExpertRoute (route_experts's), got %r" % type(route).__name__)
+
+
 def _validate_experts(x, q, scales, route, bias, gated, gather, out, device):
     import torch
     check = _pkg._check
     check(x, "x", torch.float16, ndim=2, device=device)
     x_rows, k = x.shape
+    _check_route(route)
     check(route.ids, "route.ids", torch.int32, ndim=2, device=device)
     tokens, top_k = route.ids.shape
     entries = tokens * top_k
@@ -465,6 +471,7 @@ def _validate_combine(y, route, residual, out, device):
     check = _pkg._check
     check(y, "y", torch.float16, ndim=2, device=device)
     n = y.shape[1]
+    _check_route(route)
     check(route.places, "route.places", torch.int32, ndim=2, device=device)
     tokens, top_k = route.places.shape
     check(y, "y", torch.float16, shape=(tokens * top_k, n), device=device)
