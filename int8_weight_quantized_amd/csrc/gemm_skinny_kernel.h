@@ -60,8 +60,18 @@ constexpr int kSkinnyTargetWaves = 2048; // enough in-flight loads to fill HBM
 // in LDS, and the residual is added where it is stored: one rounding.
 // GRP: a grouped product (qw_w8a16_experts); blockIdx.y is a row tile of
 // 16 MT entries of one expert, and m the expert's end.
-template <int RT, int MT, int KSPLIT, bool A8 = false, bool ZP = false, int EPI = kPlain, bool GRP = false>
-__global__ __launch_bounds__(KSPLIT * 64) void skinny_gemm_kernel(
+//
+// RW > 1: RW waves of neighbouring weight rows for each part of k, RW * KSPLIT in
+// all.  They share the activations of an iteration through LDS, each wave loading
+// its part of them: with a row block a wave, every wave reads all of the
+// activations again, which for 16 rows in fp16 and 32 weight rows are as many
+// bytes as its weights.  All waves keep step (a barrier an iteration, two tiles of
+// activations in turn), and the loads of two iterations are in flight.  Us, 4096
+// deep, 16 rows, n = 27392 (gated) / 16384 / 65024: 24.2 / 15.5 / 46.3, without
+// 30.1 / 18.1 / 55.3; 32 rows 28.1 / 18.4 / 60.5 and 34.9 / 26.4 / 72.2.  Three
+// iterations ahead were 4 to 20 % slower.
+template <int RT, int MT, int KSPLIT, bool A8 = false, bool ZP = false, int EPI = kPlain, bool GRP = false, int RW = 1>
+__global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
     const void *__restrict__ xv, const uint16_t *__restrict__ sx, const int8_t *__restrict__ q,
     const uint16_t *__restrict__ scales, const int8_t *__restrict__ zeros, OutlierList ol,
     uint16_t *__restrict__ y, int m, int n, int k, Epilogue ep, Experts ex)
@@ -69,27 +79,31 @@ __global__ __launch_bounds__(KSPLIT * 64) void skinny_gemm_kernel(
     static_assert(EPI == kPlain || !ZP, "symmetric codes");
     static_assert(EPI != kGated || RT % 2 == 0, "gate and up in pairs of tiles");
     static_assert(!GRP || (EPI != kPlain && !A8), "grouped products are W8A16 with an epilogue");
+    static_assert(RW == 1 || (EPI != kPlain && !GRP), "shared activations: products with an epilogue");
     const uint16_t *__restrict__ x = static_cast<const uint16_t *>(xv);
     using acc_t = std::conditional_t<A8, int4v, float4v>;
     // Per wave, a staging slice for the weight codes of one iteration:
     // [tile][row][256 bytes + 16 pad].  After the main loop the same memory
-    // holds the partial tiles of waves 1 .. KSPLIT-1.
+    // holds the partial tiles of the parts 1 .. KSPLIT-1.
     constexpr int kStageRow = 64 * kSkinnyUnroll + 16; // 256 codes + pad
-    constexpr int kStageBytes = KSPLIT * RT * 16 * kStageRow;
-    constexpr int kPartialBytes = (KSPLIT > 1 ? KSPLIT - 1 : 1) * RT * MT * kWave * (int)sizeof(acc_t);
+    constexpr int kStageBytes = RW * KSPLIT * RT * 16 * kStageRow;
+    constexpr int kPartialBytes = RW * (KSPLIT > 1 ? KSPLIT - 1 : 1) * RT * MT * kWave * (int)sizeof(acc_t);
     __shared__ __attribute__((aligned(16))) uint8_t smem[kStageBytes > kPartialBytes ? kStageBytes : kPartialBytes];
     // the finished tile (fp16, or fp32 with EPI), [activation row][channel], padded rows
     constexpr int kCols = EPI == kGated ? 8 * RT : 16 * RT; // columns of Y a workgroup
     using tile_t = std::conditional_t<EPI == kPlain, uint16_t, float>;
-    __shared__ __attribute__((aligned(16))) tile_t ytile[16 * MT][kCols + (EPI == kPlain ? 8 : 4)];
+    __shared__ __attribute__((aligned(16))) tile_t ytiles[RW * 16 * MT][kCols + (EPI == kPlain ? 8 : 4)];
     static_assert(kSkinnyUnroll == 4, "one iteration covers 256 codes of a row");
 
     const int lane = __lane_id();
-    const int wave = threadIdx.x / kWave;
+    const int wave_id = threadIdx.x / kWave;
+    const int wave = RW > 1 ? wave_id / RW : wave_id; // part of k
+    const int rw = RW > 1 ? wave_id % RW : 0;         // row block of the workgroup
+    auto *ytile = ytiles + rw * 16 * MT;
     const int r = lane % 16;
     const int g = lane / 16;
     const int n_out = EPI == kGated ? n / 2 : n;
-    const int n0 = blockIdx.x * kCols; // first column of Y
+    const int n0 = (blockIdx.x * RW + rw) * kCols; // first column of Y
     // weight row r16 of tile t, and whether it is one
     auto row_of = [&](int t, int r16) { return EPI == kGated ? (t & 1) * n_out + n0 + 16 * (t / 2) + r16 : n0 + 16 * t + r16; };
     auto row_in = [&](int t, int r16) { return EPI == kGated ? n0 + 16 * (t / 2) + r16 < n_out : n0 + 16 * t + r16 < n; };
@@ -172,7 +186,110 @@ __global__ __launch_bounds__(KSPLIT * 64) void skinny_gemm_kernel(
         for (int mt = 0; mt < MT; ++mt)
             acc[t][mt] = (acc_t){};
 
-    for (int s = s_begin; s < s_end; s += kSkinnyUnroll) {
+    if constexpr (RW > 1) {
+        constexpr int kElem = A8 ? 1 : 2;
+        constexpr int kXRow = 64 * kSkinnyUnroll * kElem + 16; // an iteration's activations of a row + pad
+        constexpr int kXTile = 16 * MT * kXRow;
+        constexpr int kXLanes = 4 * kSkinnyUnroll * kElem;     // lanes a row, 16 bytes each
+        constexpr int kXLoads = 16 * MT * kXLanes / (RW * kWave);
+        static_assert(kXLoads * RW * kWave == 16 * MT * kXLanes, "a whole number of loads");
+        __shared__ __attribute__((aligned(16))) uint8_t xtiles[KSPLIT * 2 * kXTile];
+        uint8_t *slice = smem + wave_id * RT * 16 * kStageRow;
+        uint8_t *xtile = xtiles + wave * 2 * kXTile;
+        u32x4_t raw[2][4][RT], xraw[2][kXLoads];
+        const uint8_t *xp[kXLoads];
+        bool xin[kXLoads];
+        const int xpiece = lane % kXLanes; // of the row
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) {
+            const int col = m0 + (i * RW * kWave + rw * kWave + lane) / kXLanes;
+            xin[i] = col < m;
+            xp[i] = static_cast<const uint8_t *>(xv) + (int64_t)(xin[i] ? col : 0) * k * kElem + 16 * xpiece;
+        }
+        // Both loads leave what is behind the part's end, k, m or n zero.
+        auto load = [&](int d, int s) {
+#pragma unroll
+            for (int i = 0; i < kXLoads; ++i) {
+                const int kk = s * 64 + 16 / kElem * xpiece;
+                xraw[d][i] = (u32x4_t){0u, 0u, 0u, 0u};
+                if (xin[i] && kk < 64 * s_end && kk < k)
+                    xraw[d][i] = *reinterpret_cast<const u32x4_t *>(xp[i] + (int64_t)s * 64 * kElem);
+            }
+            const int kl = s * 64 + 16 * (lane % 16);
+            const bool okl = kl < 64 * s_end && kl < k;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = row_of(t, 4 * i + lane / 16);
+                    raw[d][i][t] = (u32x4_t){0u, 0u, 0u, 0u};
+                    if (okl && row_in(t, 4 * i + lane / 16))
+                        raw[d][i][t] = __builtin_nontemporal_load(
+                            reinterpret_cast<const u32x4_t *>(q + (int64_t)row * k + kl));
+                }
+        };
+        // (as many for every wave: the longest part's)
+        const int rounds = ((steps_total + KSPLIT - 1) / KSPLIT + kSkinnyUnroll - 1) / kSkinnyUnroll;
+        load(0, s_begin);
+        load(1, s_begin + kSkinnyUnroll);
+        for (int i0 = 0; i0 < rounds; i0 += 2) {
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                if (i0 + d >= rounds)
+                    break;
+                uint8_t *xs = xtile + d * kXTile;
+#pragma unroll
+                for (int i = 0; i < kXLoads; ++i)
+                    *reinterpret_cast<u32x4_t *>(xs + (i * RW * kWave + rw * kWave + lane) / kXLanes * kXRow + 16 * xpiece) =
+                        xraw[d][i];
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<u32x4_t *>(slice + (t * 16 + 4 * i + lane / 16) * kStageRow + 16 * (lane % 16)) =
+                            raw[d][i][t];
+                __builtin_amdgcn_sched_barrier(0); // (the loads into these registers not before)
+                load(d, s_begin + (i0 + d + 2) * kSkinnyUnroll);
+                // This tile of activations was read two iterations ago, before
+                // the barrier of the last one.  The asm waits for LDS alone: the
+                // loads stay in flight.
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+                for (int u = 0; u < kSkinnyUnroll; ++u) {
+                    u32x4_t xa[MT], xb[MT];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint8_t *p = xs + (16 * mt + r) * kXRow + (64 * u + 16 * g) * kElem;
+                        xa[mt] = *reinterpret_cast<const u32x4_t *>(p);
+                        if constexpr (!A8)
+                            xb[mt] = *reinterpret_cast<const u32x4_t *>(p + 16);
+                    }
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        const u32x4_t w = *reinterpret_cast<const u32x4_t *>(slice + (t * 16 + r) * kStageRow + 64 * u + 16 * g);
+                        if constexpr (A8) {
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+                                acc[t][mt] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                    __builtin_bit_cast(int4v, w), __builtin_bit_cast(int4v, xa[mt]), acc[t][mt], 0, 0, 0);
+                        } else {
+                            const half8_t a0 = i8x8_to_half8(w.x, w.y, zbias[t]);
+                            const half8_t a1 = i8x8_to_half8(w.z, w.w, zbias[t]);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                acc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, __builtin_bit_cast(half8_t, xa[mt]),
+                                                                                   acc[t][mt], 0, 0, 0);
+                                acc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, __builtin_bit_cast(half8_t, xb[mt]),
+                                                                                   acc[t][mt], 0, 0, 0);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    for (int s = s_begin; RW == 1 && s < s_end; s += kSkinnyUnroll) {
         u32x4_t wv[kSkinnyUnroll][RT];
         u32x4_t xa[kSkinnyUnroll][MT], xb[kSkinnyUnroll][MT];
         // Activation operands.  For the fp16 kernel with one activation
@@ -291,14 +408,14 @@ __global__ __launch_bounds__(KSPLIT * 64) void skinny_gemm_kernel(
     }
 
     if (KSPLIT > 1) {
-        acc_t *partial = reinterpret_cast<acc_t *>(smem); // [KSPLIT-1][RT][MT][kWave]
+        acc_t *partial = reinterpret_cast<acc_t *>(smem); // [KSPLIT-1][RW][RT][MT][kWave]
         __syncthreads(); // every wave is done with its staging slice
         if (wave > 0) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    partial[(((wave - 1) * RT + t) * MT + mt) * kWave + lane] = acc[t][mt];
+                    partial[((((wave - 1) * RW + rw) * RT + t) * MT + mt) * kWave + lane] = acc[t][mt];
         }
         __syncthreads();
         if (wave != 0)
@@ -309,7 +426,7 @@ __global__ __launch_bounds__(KSPLIT * 64) void skinny_gemm_kernel(
             for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    acc[t][mt] += partial[((w * RT + t) * MT + mt) * kWave + lane];
+                    acc[t][mt] += partial[(((w * RW + rw) * RT + t) * MT + mt) * kWave + lane];
     }
     if constexpr (EPI == kPlain) {
         // lane holds channels n0 + 16 t + 4 g + i (i = 0..3) of activation row

@@ -92,6 +92,16 @@ def test_skinny(m, n, k, a8, gated):
     check(8, m, n, k, a8=a8, act="silu" if gated else None, gated=gated, path="skinny", dtype=BF16 if a8 and gated else F16)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("a8", [False, True])
+@pytest.mark.parametrize("m,n,k", [(5, 12290, 16), (16, 12346, 272), (9, 12354, 4112), (8, 24706, 528), (16, 24578, 48), (17, 24600, 2048),
+                                   (32, 24578, 2064), (24, 12354, 4112), (12, 33026, 80), (31, 33002, 2304)])
+def test_skinny_wide(m, n, k, a8, gated):
+    """Many weight rows: waves that share the activations, one and two tiles of
+    them, parts of k of different lengths or none, the last row block cut off."""
+    check(21, m, n, k, a8=a8, act="silu" if gated else None, gated=gated, path="skinny", dtype=BF16 if a8 and gated else F16)
+
+
 TILES = [256256, 256128, 256064, 128128, 128064]
 
 
