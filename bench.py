@@ -56,9 +56,9 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "hbm_traffic.json")
 CSRC = os.path.join(ROOT, "int8_weight_quantized_amd", "csrc")
 KERNEL_SOURCES = {
     "quantize": ["quantize.hip", "qw_device.h"],
-    "gemv": ["gemv.hip", "qw_device.h"],
-    "mfma": ["gemm_mfma.hip", "qw_device.h"],
-    "skinny": ["gemm_skinny.hip", "qw_device.h"],
+    "gemv": ["gemv.hip", "qw_device.h", "epilogue_device.h"],
+    "mfma": ["gemm_mfma.hip", "gemm_mfma_kernels.h", "qw_device.h", "epilogue_device.h"],
+    "skinny": ["gemm_skinny.hip", "gemm_skinny_kernel.h", "qw_device.h", "epilogue_device.h"],
 }
 
 

@@ -30,9 +30,10 @@
  *   - Arguments are checked on the host before anything is enqueued; on
  *     any error nothing is launched and no output byte is written.
  *   - Results are deterministic: every floating-point reduction runs in a
- *     fixed order.  The only atomics are integer additions into the
- *     percentile quantizer's LDS histogram, whose counts do not depend on
- *     the order of the additions; no global-memory atomics are used.
+ *     fixed order.  The only atomics are integer additions in LDS (the
+ *     percentile quantizer's histogram, qw_route_experts's counts), whose
+ *     sums do not depend on the order of the additions; no global-memory
+ *     atomics are used.
  *   - Not safe to call with overlapping input and output buffers
  *     (rejected with QW_ERROR_INVALID_VALUE when detected).
  */
