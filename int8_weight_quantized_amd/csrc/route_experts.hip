@@ -127,10 +127,6 @@ __device__ __forceinline__ void static_for(F &&f)
 struct Key {
     uint32_t hi, lo;
 };
-__device__ __forceinline__ bool operator>(const Key &a, const Key &b)
-{
-    return ((uint64_t)a.hi << 32 | a.lo) > ((uint64_t)b.hi << 32 | b.lo);
-}
 __device__ __forceinline__ Key key_of(float v) // of a number, or -infinity
 {
     const uint32_t b = __builtin_bit_cast(uint32_t, v);
@@ -227,8 +223,9 @@ __device__ __forceinline__ float logit(const void *logits, int64_t at)
 
 __device__ __forceinline__ float eligible(float l)
 {
-    // a NaN is not; infinity counts as the largest number
-    return l > -__builtin_inff() ? fminf(l, 3.402823466e38f) : -__builtin_inff();
+    // a NaN is not; infinity counts as the largest number, and -0 as 0 (keys tell
+    // them apart)
+    return l > -__builtin_inff() ? fminf(l, 3.402823466e38f) + 0.0f : -__builtin_inff();
 }
 
 // Lanes that share a group of experts: neighbours, a power of two.
@@ -431,6 +428,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t token, bool l
     if (a.bias) {
         const uint32_t bits = most_of<L>(__builtin_bit_cast(uint32_t, size_b)); // (not negative: ordered as it is)
         error = 0x1p-18f * (1.0f + __builtin_bit_cast(float, bits));
+        slow = slow || !(error < 0x1p60f); // (an infinite bias, or one whose sums may be, has no bounds)
     }
     if (a.groups > 1 && !slow) {
         const int size = a.experts / a.groups, share = lanes_a_group<L>(a), group = lane / share;

@@ -103,6 +103,31 @@ def test_masked_experts():
     assert (r.ids[:, 4:] == -1).all()
 
 
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_large_biases(scoring, groups):
+    """One of infinity puts an expert before all others, and the largest numbers
+    lose the scores' bits and overflow as a group's sum, in fp32."""
+    for values in ((INF, 0.0, INF, -INF), (3e38, 3e38, -3e38, 1e30), (INF, 3e38, NAN, -3e38)):
+        bias = normal(15, 1, 32, size=0.05)[0]
+        for i, v in enumerate(values):
+            bias[5 + 7 * i] = v
+        for top_k in (1, 2, 6):
+            check(normal(16, 40, 32), top_k, bias=bias, scoring=scoring, groups=groups, top_groups=max(1, groups // 2))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_signed_zeros_tie(groups, dtype):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(17)
+    x = torch.zeros(60, 64, dtype=dtype, device="cuda")
+    x[torch.rand(x.shape, generator=gen, device="cuda") < 0.5] = -0.0
+    x[::2, 10] = 1.0
+    check(x, 5, groups=groups, top_groups=max(1, groups // 2))
+    check(x, 5, scoring="sigmoid", groups=groups, top_groups=1)
+
+
 @pytest.mark.parametrize("tokens", [1000, 4096, 4097, 9001])
 def test_many_tokens(tokens):
     check(normal(12, tokens, 64, BF16), 4)
