@@ -889,23 +889,25 @@ QW_API qw_status qw_add_rms_norm_quantize(const void *x, int64_t x_stride, const
  *   workspace   qw_w8a16_linear_workspace() bytes, or null
  *
  * The kernels and their choice are qw_w8a16_gemm's, tuning records included.
- * Where their grid would leave much of the chip idle, and there is a workspace,
- * the reduction is split in parts whose sums are kept in it and added up, in
+ * Where their grid would leave much of the chip idle and there is a workspace,
+ * the reduction may be split in parts, whose sums are kept in it and added up, in
  * order, by a second launch.
  * Accuracy: the sum as there, the activations within 2^-17 relative (of v for
  * the gelus' and silu's negative tails beyond -6).
  * qw_w8a16_linear_path forces a kernel, for QW_PATH_MFMA with a nonzero `tile`
- * that tile (as qw_w8a16_gemm_tile), and with tile 256256 the number of parts
- * (`splits`, else 1; workspace: 262144 bytes for each part of each 256 x 256
- * tile).
+ * that tile (as qw_w8a16_gemm_tile), and with tile 256256 or QW_PATH_SKINNY the
+ * number of parts (`splits`, else 1).  Their workspace is for each part 262144
+ * bytes for each 256 x 256 tile of v, or 4 bytes for each element of v with m
+ * rounded up to 16 (to 32 for 17 to 32 rows and k >= 2048) and n to 64 (gated: 128).
  *
  * Errors: as qw_w8a16_gemm_path, plus QW_ERROR_INVALID_VALUE for an unknown
  * activation, gated not 0 or 1 or with an odd n, an unknown tile or one without
- * QW_PATH_MFMA, splits below 1 or above 64 or without tile 256256, a workspace
+ * QW_PATH_MFMA, splits below 1 or above 64 or above 1 with neither of these, a workspace
  * that is too small or overlaps anything, y overlapping bias, or residual at
  * another place than its own, and QW_ERROR_UNSUPPORTED where a forced kernel
  * does not take the sizes: QW_PATH_GEMV with m > 2, or gated with k > 8192,
- * QW_PATH_MFMA gated with n * k >= 2^32, k < 64 * splits.
+ * QW_PATH_MFMA gated with n * k >= 2^32, k < 64 * splits, parts of QW_PATH_SKINNY
+ * with k above 2^30.
  *
  * qw_w8a16_linear_workspace -- workspace bytes for these sizes on the current
  * device (0: none needed), -1 for sizes that the call rejects.

@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kSkinnyPartsMaxK = 1 << 30; // (its loads ahead count past k in 32 bits)
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
@@ -44,9 +45,25 @@ int split_parts(int64_t m, int64_t n, int64_t k, bool gated)
     return (int)(cus / tiles < 8 ? cus / tiles : 8);
 }
 
+// The same for a few rows on the skinny kernel: as many parts as give each CU a
+// workgroup of 64 weight rows (gated: 128) that share the activations.  The second
+// launch costs about 3 us, and what is saved are reads of all activations for
+// every 16 or 32 weight rows, so these decide.  Us without / with parts: fp16, 16
+// rows (activations of 256 KB from k = 8192) 4096 x 4096 9 / 10, 2048 x 8192 12.5 /
+// 10.3, 8192 x 8192 22 / 18, 4096 x 13696 22 / 19, 8192 x 28672 54 / 43; 8 rows 4096 x
+// 13696 16 / 18; 32 rows 4096 x 4096 12.9 / 11.5, 4096 x 13696 33 / 21, gated 16384 x
+// 4096 25 / 23; W8A8 32 rows 4096 x 4096 10.1 / 10.4, 4096 x 13696 23 / 20.
+int skinny_parts(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
+{
+    const int64_t wide = gated ? 128 : 64, tiles = (n + wide - 1) / wide, cus = qw::device_cu_count();
+    if (m <= 4 || m > 32 || m * k * (a8 ? 1 : 2) < (1 << 18) || k > kSkinnyPartsMaxK || 2 * tiles > cus)
+        return 1;
+    return (int)(cus / tiles < 8 ? cus / tiles : 8);
+}
+
 // The kernel, tile and parts of a linear call: a tuning record of the plain
-// product's bucket, else its rule, where the kernel takes the sizes; without a
-// record a split ping-pong grid where that gains.
+// product's bucket, else its rule, where the kernel takes the sizes; parts for the
+// skinny kernel, and without a record for a ping-pong grid, where they gain.
 struct LinearPlan {
     int path, tile, splits;
 };
@@ -63,6 +80,8 @@ LinearPlan plan_linear(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
         p.path = QW_PATH_SKINNY;
     if (p.path != QW_PATH_MFMA || (p.tile == 256256 && k > qw::kPingPongMaxK) || !known_tile(p.tile, a8))
         p.tile = 0;
+    if (p.path == QW_PATH_SKINNY)
+        p.splits = skinny_parts(m, n, k, gated, a8);
     // (rounding m up to 256 rows costs at most a tenth over 64, as for the
     // ping-pong tile without a split)
     const int64_t rows256 = (m + 255) / 256 * 256, rows64 = (m + 63) / 64 * 64;
@@ -74,6 +93,11 @@ LinearPlan plan_linear(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
     return p;
 }
 
+int64_t split_bytes(const LinearPlan &p, int64_t m, int64_t n, int64_t k, bool gated)
+{
+    return p.path == QW_PATH_SKINNY ? qw::skinny_parts_bytes(m, n, k, gated, p.splits) : qw::mfma_split_bytes(m, n, p.splits);
+}
+
 int64_t linear_workspace(int64_t m, int64_t n, int64_t k, int gated, bool a8)
 {
     if (m < 0 || n < 0 || k <= 0 || (gated != 0 && gated != 1) || (gated && n % 2) || k % 16 != 0 || m > kMaxDim || n > kMaxDim ||
@@ -82,7 +106,7 @@ int64_t linear_workspace(int64_t m, int64_t n, int64_t k, int gated, bool a8)
     if (m == 0 || n == 0)
         return 0;
     const LinearPlan p = plan_linear(m, n, k, gated != 0, a8);
-    return p.splits > 1 ? qw::mfma_split_bytes(m, n, p.splits) : 0;
+    return p.splits > 1 ? split_bytes(p, m, n, k, gated != 0) : 0;
 }
 
 qw_status linear(qw::LinearArgs a, int dtype, int gated, LinearPlan p, void *workspace, int64_t workspace_bytes, void *stream)
@@ -92,7 +116,7 @@ qw_status linear(qw::LinearArgs a, int dtype, int gated, LinearPlan p, void *wor
         return QW_ERROR_INVALID_VALUE;
     if (p.tile != 0 && (p.path != QW_PATH_MFMA || !known_tile(p.tile, a8)))
         return QW_ERROR_INVALID_VALUE;
-    if (p.splits < 1 || p.splits > 64 || (p.splits > 1 && p.tile != 256256) || workspace_bytes < 0 ||
+    if (p.splits < 1 || p.splits > 64 || (p.splits > 1 && p.tile != 256256 && p.path != QW_PATH_SKINNY) || workspace_bytes < 0 ||
         (workspace == nullptr && workspace_bytes > 0))
         return QW_ERROR_INVALID_VALUE;
     if (a.m < 0 || a.n < 0 || a.k <= 0 || (gated != 0 && gated != 1) || (gated && a.n % 2) ||
@@ -120,7 +144,7 @@ qw_status linear(qw::LinearArgs a, int dtype, int gated, LinearPlan p, void *wor
             p.splits = 1, p.tile = 0; // (a caller may do without)
     }
     if (p.splits > 1) {
-        const int64_t need = qw::mfma_split_bytes(a.m, a.n, p.splits);
+        const int64_t need = split_bytes(p, a.m, a.n, a.k, a.gated);
         if (workspace == nullptr || workspace_bytes < need)
             return QW_ERROR_INVALID_VALUE;
         if (off16(workspace))
@@ -139,9 +163,9 @@ qw_status linear(qw::LinearArgs a, int dtype, int gated, LinearPlan p, void *wor
                                                 a.k, s));
     }
     if (p.path == QW_PATH_SKINNY) {
-        if (a.m > 16 * 65535)
+        if (a.m > 16 * 65535 || (p.splits > 1 && (a.k < 64 * p.splits || a.k > kSkinnyPartsMaxK)))
             return QW_ERROR_UNSUPPORTED;
-        return status_of(qw::launch_skinny_linear(a, s));
+        return status_of(p.splits > 1 ? qw::launch_skinny_parts(p.splits, a, workspace, s) : qw::launch_skinny_linear(a, s));
     }
     if (!qw::mfma_linear_supported(a.n, a.k, a.gated) || (p.tile == 256256 && a.k > qw::kPingPongMaxK) ||
         (p.splits > 1 && a.k < 64 * p.splits))

@@ -14,12 +14,12 @@ hipError_t launch_cfg(const void *x, const uint16_t *sx, const int8_t *q, const 
     if constexpr (!A8) {
         if (zeros != nullptr) {
             hipLaunchKernelGGL((skinny_gemm_kernel<RT, MT, KSPLIT, false, true>), grid, dim3(KSPLIT * kWave), 0,
-                               stream, x, sx, q, scales, zeros, ol, y, (int)m, (int)n, (int)k, Epilogue{}, Experts{});
+                               stream, x, sx, q, scales, zeros, ol, y, (int)m, (int)n, (int)k, Epilogue{}, Experts{}, nullptr, 1);
             return hipGetLastError();
         }
     }
     hipLaunchKernelGGL((skinny_gemm_kernel<RT, MT, KSPLIT, A8>), grid, dim3(KSPLIT * kWave), 0, stream,
-                       x, sx, q, scales, zeros, ol, y, (int)m, (int)n, (int)k, Epilogue{}, Experts{});
+                       x, sx, q, scales, zeros, ol, y, (int)m, (int)n, (int)k, Epilogue{}, Experts{}, nullptr, 1);
     return hipGetLastError();
 }
 

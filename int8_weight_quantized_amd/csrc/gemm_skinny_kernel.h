@@ -70,16 +70,23 @@ constexpr int kSkinnyTargetWaves = 2048; // enough in-flight loads to fill HBM
 // deep, 16 rows, n = 27392 (gated) / 16384 / 65024: 24.2 / 15.5 / 46.3, without
 // 30.1 / 18.1 / 55.3; 32 rows 28.1 / 18.4 / 60.5 and 34.9 / 26.4 / 72.2.  Three
 // iterations ahead were 4 to 20 % slower.
-template <int RT, int MT, int KSPLIT, bool A8 = false, bool ZP = false, int EPI = kPlain, bool GRP = false, int RW = 1>
+//
+// PART (with RW > 1): the reduction split over `parts` workgroups too (blockIdx.z).
+// kParts leaves each one's sums in `partial`, and kJoin, a launch of its own with
+// the same RT, MT and RW, adds them in the parts' order for the epilogue.
+enum { kWhole = 0, kParts = 1, kJoin = 2 };
+template <int RT, int MT, int KSPLIT, bool A8 = false, bool ZP = false, int EPI = kPlain, bool GRP = false, int RW = 1,
+          int PART = kWhole>
 __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
     const void *__restrict__ xv, const uint16_t *__restrict__ sx, const int8_t *__restrict__ q,
     const uint16_t *__restrict__ scales, const int8_t *__restrict__ zeros, OutlierList ol,
-    uint16_t *__restrict__ y, int m, int n, int k, Epilogue ep, Experts ex)
+    uint16_t *__restrict__ y, int m, int n, int k, Epilogue ep, Experts ex, void *__restrict__ partial_sums, int parts)
 {
     static_assert(EPI == kPlain || !ZP, "symmetric codes");
     static_assert(EPI != kGated || RT % 2 == 0, "gate and up in pairs of tiles");
     static_assert(!GRP || (EPI != kPlain && !A8), "grouped products are W8A16 with an epilogue");
     static_assert(RW == 1 || (EPI != kPlain && !GRP), "shared activations: products with an epilogue");
+    static_assert(PART == kWhole || (RW > 1 && (PART == kParts || KSPLIT == 1)), "parts of wide workgroups");
     const uint16_t *__restrict__ x = static_cast<const uint16_t *>(xv);
     using acc_t = std::conditional_t<A8, int4v, float4v>;
     // Per wave, a staging slice for the weight codes of one iteration:
@@ -127,8 +134,10 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
     }
 
     const int steps_total = (k + 63) / 64;
-    const int s_begin = (int)(((int64_t)wave * steps_total) / KSPLIT);
-    const int s_end = (int)(((int64_t)(wave + 1) * steps_total) / KSPLIT);
+    const int s_first = PART == kParts ? (int)((int64_t)blockIdx.z * steps_total / parts) : 0;
+    const int steps = PART == kParts ? (int)((int64_t)(blockIdx.z + 1) * steps_total / parts) - s_first : steps_total;
+    const int s_begin = s_first + (int)(((int64_t)wave * steps) / KSPLIT);
+    const int s_end = s_first + (int)(((int64_t)(wave + 1) * steps) / KSPLIT);
 
     const int8_t *qrow[RT];
     bool row_ok[RT];
@@ -186,7 +195,19 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
         for (int mt = 0; mt < MT; ++mt)
             acc[t][mt] = (acc_t){};
 
-    if constexpr (RW > 1) {
+    // this lane's sums of tile (t, mt) of part p
+    auto sums_of = [&](int p, int t, int mt) {
+        const int64_t block = ((int64_t)p * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+        return static_cast<acc_t *>(partial_sums) + (block * (RW * RT * MT) + (rw * RT + t) * MT + mt) * kWave + lane;
+    };
+    if constexpr (PART == kJoin) {
+        for (int p = 0; p < parts; ++p)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    acc[t][mt] += *sums_of(p, t, mt);
+    } else if constexpr (RW > 1) {
         constexpr int kElem = A8 ? 1 : 2;
         constexpr int kXRow = 64 * kSkinnyUnroll * kElem + 16; // an iteration's activations of a row + pad
         constexpr int kXTile = 16 * MT * kXRow;
@@ -229,7 +250,7 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
                 }
         };
         // (as many for every wave: the longest part's)
-        const int rounds = ((steps_total + KSPLIT - 1) / KSPLIT + kSkinnyUnroll - 1) / kSkinnyUnroll;
+        const int rounds = ((steps + KSPLIT - 1) / KSPLIT + kSkinnyUnroll - 1) / kSkinnyUnroll;
         load(0, s_begin);
         load(1, s_begin + kSkinnyUnroll);
         for (int i0 = 0; i0 < rounds; i0 += 2) {
@@ -285,6 +306,8 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
                         }
                     }
                 }
+                // (the next codes go into the slice behind these reads, as below)
+                __builtin_amdgcn_wave_barrier();
             }
         }
     }
@@ -427,6 +450,14 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     acc[t][mt] += partial[(((w * RW + rw) * RT + t) * MT + mt) * kWave + lane];
+    }
+    if constexpr (PART == kParts) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                *sums_of(blockIdx.z, t, mt) = acc[t][mt];
+        return;
     }
     if constexpr (EPI == kPlain) {
         // lane holds channels n0 + 16 t + 4 g + i (i = 0..3) of activation row

@@ -181,6 +181,10 @@ bool gemv_linear_supported(int64_t m, int64_t k, bool gated);
 hipError_t launch_gemv_linear(const uint16_t *x, const int8_t *q, const uint16_t *scales, const Epilogue &ep, bool gated,
                               uint16_t *y, int64_t m, int64_t n, int64_t k, hipStream_t stream);
 hipError_t launch_skinny_linear(const LinearArgs &a, hipStream_t stream);
+// The same with the reduction in `parts` parts of 64 steps or more, whose sums
+// take skinny_parts_bytes() of workspace; k up to 2^30.
+int64_t skinny_parts_bytes(int64_t m, int64_t n, int64_t k, bool gated, int parts);
+hipError_t launch_skinny_parts(int parts, const LinearArgs &a, void *workspace, hipStream_t stream);
 // Whether the MFMA kernels take these sizes, and their launch (tile as in
 // mfma_tile_choice).
 bool mfma_linear_supported(int64_t n, int64_t k, bool gated);

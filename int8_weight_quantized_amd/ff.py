@@ -266,7 +266,7 @@ def w8a16_linear(x, q, scales, bias=None, activation=None, gated: bool = False, 
     if index != _kv._current_device():
         return _pkg._on_device(index, w8a16_linear, x, q, scales, bias, activation, gated, residual, out)
     lib = _pkg.library()
-    _held, ws, size = _workspace(lib.qw_w8a16_linear_workspace(m, n, k, 1 if gated else 0) if m > 16 else 0, x.device)
+    _held, ws, size = _workspace(lib.qw_w8a16_linear_workspace(m, n, k, 1 if gated else 0) if m > 4 else 0, x.device)
     status = lib.qw_w8a16_linear(
         x.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(bias), act, 1 if gated else 0, _ptr(residual), y.data_ptr(), m, n, k,
         ws, size, _kv._raw_stream(index))
@@ -309,7 +309,7 @@ def w8a8_linear(qx, sx, q, scales, bias=None, activation=None, gated: bool = Fal
     if index != _kv._current_device():
         return _pkg._on_device(index, w8a8_linear, qx, sx, q, scales, bias, activation, gated, residual, dtype, out)
     lib = _pkg.library()
-    _held, ws, size = _workspace(lib.qw_w8a8_linear_workspace(m, n, k, 1 if gated else 0) if m > 16 else 0, qx.device)
+    _held, ws, size = _workspace(lib.qw_w8a8_linear_workspace(m, n, k, 1 if gated else 0) if m > 4 else 0, qx.device)
     status = lib.qw_w8a8_linear(
         qx.data_ptr(), sx.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(bias), act, 1 if gated else 0, _ptr(residual), code,
         y.data_ptr(), m, n, k, ws, size, _kv._raw_stream(index))

@@ -43,7 +43,7 @@ def test_a_route_is_needed(devices):
 
 def test_workspaces_are_asked_for(monkeypatch):
     """A product whose reduction the library splits takes the bytes it names;
-    16 rows and fewer never do, and are not asked about."""
+    four rows and fewer never do, and are not asked about."""
     asked, given = [], []
 
     class Library:
@@ -61,7 +61,7 @@ def test_workspaces_are_asked_for(monkeypatch):
     monkeypatch.setattr(qw.kv, "_current_device", lambda: 1, raising=False)
     monkeypatch.setattr(qw.kv, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(qw, "library", Library)
-    for m, k in ((16, 64), (17, 64), (17, 32)):
+    for m, k in ((4, 64), (5, 64), (5, 32)):
         qw.w8a16_linear(second((m, k)), second((8, k), I8), second(8), gated=True)
-    assert asked == [(17, 8, 64, 1), (17, 8, 32, 1)]
+    assert asked == [(5, 8, 64, 1), (5, 8, 32, 1)]
     assert given[0] == given[2] == (None, 0) and given[1][0] and given[1][1] == 4096

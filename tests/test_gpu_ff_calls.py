@@ -74,6 +74,7 @@ class Sparse(Dense):
 STEPS = {
     "one token": lambda: Dense(1, 512, 1024, False),
     "tokens": lambda: Dense(40, 512, 1024, False),
+    "few rows' parts": lambda: Dense(16, 512, 8192, False),
     "split": lambda: Dense(256, 512, 8192, False),
     "codes": lambda: Dense(40, 512, 1024, True),
     "split codes": lambda: Dense(250, 512, 8192, True),
@@ -85,6 +86,7 @@ STEPS = {
 
 def test_the_splits_are_reached():
     lib = qw.library()
+    assert lib.qw_w8a16_linear_workspace(16, 512, 8192, 0) > 0
     assert lib.qw_w8a16_linear_workspace(256, 512, 8192, 0) > 0 and lib.qw_w8a8_linear_workspace(250, 512, 8192, 0) > 0
 
 
@@ -113,7 +115,8 @@ def test_replayed(name):
             assert torch.equal(step(), eager[seed])
 
 
-@pytest.mark.parametrize("first,second", [("split", "split codes"), ("experts", "many tokens' experts")])
+@pytest.mark.parametrize("first,second", [("split", "split codes"), ("experts", "many tokens' experts"),
+                                          ("few rows' parts", "split")])
 def test_two_graphs_of_one_pool(first, second):
     """Graphs that share their memory, and so their workspaces, replayed in
     turn on one stream."""
@@ -135,7 +138,8 @@ def test_two_graphs_of_one_pool(first, second):
             assert torch.equal(out, w)
 
 
-@pytest.mark.parametrize("a,b", [("split", "split codes"), ("experts", "many tokens' experts"), ("tokens", "one token's experts")])
+@pytest.mark.parametrize("a,b", [("split", "split codes"), ("experts", "many tokens' experts"), ("tokens", "one token's experts"),
+                                 ("few rows' parts", "split codes")])
 def test_two_streams(a, b):
     """Steps side by side on two streams, each with its own workspaces."""
     steps = [STEPS[a](), STEPS[b]()]

@@ -130,6 +130,26 @@ def test_split(m, n, k, splits, a8, gated):
           splits=splits)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("a8", [False, True])
+@pytest.mark.parametrize("m,n,k,splits", [(1, 2, 128, 2), (5, 66, 400, 3), (16, 264, 1088, 8), (17, 130, 2064, 5), (32, 514, 4112, 4), (40, 70, 512, 8),
+                                          (9, 1024, 8192, 8), (31, 192, 4096, 64)])
+def test_skinny_parts(m, n, k, splits, a8, gated):
+    check(22, m, n, k, a8=a8, act="silu" if gated else "relu", gated=gated, path="skinny", splits=splits, dtype=BF16 if a8 and gated else F16)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m,n,k", [(9, 1024, 16400), (16, 4098, 8192), (32, 2050, 4096), (32, 8192, 4112)])
+def test_skinny_parts_by_itself(m, n, k, gated):
+    """Few rows, few channels and long rows are split, and the parts change the
+    sum by fp32's roundings alone (here: not at all)."""
+    assert qw.library().qw_w8a16_linear_workspace(m, n, k, int(gated)) > 0
+    x, _, q, s, b, r = operands(23, m, n, k, gated=gated)
+    split = qw.w8a16_linear(x, q, s, bias=b, activation="silu", gated=gated, residual=r)
+    whole = call(x, None, q, s, b, r, "silu", gated, path="skinny")
+    assert torch.equal(split, whole)
+
+
 @pytest.mark.parametrize("m,n,k", [(512, 1024, 8192), (250, 520, 13696), (700, 2048, 9232)])
 def test_split_by_itself(m, n, k):
     """Sizes that the calls split on their own."""
