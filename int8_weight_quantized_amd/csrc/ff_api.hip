@@ -30,17 +30,17 @@ bool known_tile(int tile, bool a8)
 // Parts to split the reduction of a ping-pong grid into: as many as fill the
 // CUs, at most 8, where its tiles cover at most half of them and the reduction
 // is long.  The accumulators' way to memory and back, and the second launch,
-// cost some 30 to 50 us with all CUs at work.  Us, best tile without a split /
-// split, k = 8192, 11008, 13696, 20480, n = 4096: W8A8 256 rows 60 / 52, 77 / 58,
-// 93 / 61, 143 / 78; 512 rows 63 / 59, 80 / 66, 93 / 69, 146 / 86; 2048 rows 116 /
-// 98, 149 / 117, 176 / 134, 270 / 187; W8A16 512 rows 71 / 69, 111 / 79, 140 / 87,
-// 206 / 107; 2048 rows 142 / 141, 186 / 177, 229 / 211, 336 / 298.  With k = 4096
-// no part count gained: W8A8 512 rows 26 / 43, 2048 rows 55 / 66.
-int split_parts(int64_t m, int64_t n, int64_t k, bool gated)
+// cost some 20 to 40 us with all CUs at work.  Us, best tile without a split /
+// split, n = 4096, k = 4096, 6144, 8192, 13696, 20480: W8A8 256 rows 25 / 33, 37 /
+// 31, 61 / 35, 93 / 44, 143 / 61; 512 rows 26 / 45, 39 / 48, 63 / 54, 94 / 57, 146 / 73;
+// 2048 rows 57 / 60, 90 / 78, 112 / 92, 173 / 131, 268 / 184; W8A16 256 rows 34 / 36,
+// 47 / 36, 70 / 42, 139 / 55, 206 / 75; 512 rows 35 / 44, 56 / 51, 71 / 57, 139 / 75,
+// 206 / 96; 2048 rows 82 / 85, 119 / 111, 151 / 137, 245 / 211, 361 / 301.
+int split_parts(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
 {
     const int64_t columns = gated ? n / 2 : n, bn = gated ? 128 : 256;
     const int64_t tiles = ((m + 255) / 256) * ((columns + bn - 1) / bn), cus = qw::device_cu_count();
-    if (k < 8192 || 2 * tiles > cus)
+    if (k < (a8 ? 8192 : 6144) || 2 * tiles > cus)
         return 1;
     return (int)(cus / tiles < 8 ? cus / tiles : 8);
 }
@@ -86,7 +86,7 @@ LinearPlan plan_linear(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
     // ping-pong tile without a split)
     const int64_t rows256 = (m + 255) / 256 * 256, rows64 = (m + 63) / 64 * 64;
     if (p.path == QW_PATH_MFMA && p.tile == 0 && k <= qw::kPingPongMaxK && 10 * rows256 <= 11 * rows64) {
-        p.splits = split_parts(m, n, k, gated);
+        p.splits = split_parts(m, n, k, gated, a8);
         if (p.splits > 1)
             p.tile = 256256;
     }

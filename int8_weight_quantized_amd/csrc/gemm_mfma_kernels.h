@@ -1488,8 +1488,10 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
 }
 
 // The sum of the split products' accumulators, copy by copy, and the epilogue:
-// a workgroup for each of a tile's two wave groups (128 rows), whose threads
-// take the registers that the threads of the same place left.
+// a workgroup for 32 rows of a tile, whose threads take the registers that the
+// threads of the same place left.  Bound by memory; with 128 rows a workgroup
+// there were too few loads in flight (two copies of 2039 x 4096 with a residual:
+// 27 us, so 20, 5.0 TB/s).
 template <bool A8, int EPI>
 __global__ __launch_bounds__(pp::kThreads / 2) void mfma_join_kernel(const u32x4_t *__restrict__ partial, int splits,
                                                                      const uint16_t *__restrict__ sx,
@@ -1502,36 +1504,35 @@ __global__ __launch_bounds__(pp::kThreads / 2) void mfma_join_kernel(const u32x4
     constexpr int kCols = EPI == kGated ? kBN / 2 : kBN; // columns of Y a tile
     constexpr int kRow = kCols * 2 + 16, kPieces = kCols / 8;
     const int n_out = EPI == kGated ? n / 2 : n;
-    __shared__ __attribute__((aligned(16))) uint8_t image[kGroupRows * kRow];
+    constexpr int kRows = 32;
+    __shared__ __attribute__((aligned(16))) uint8_t image[kRows * kRow];
     __shared__ __attribute__((aligned(16))) float scale_lds[kBN];
     __shared__ __attribute__((aligned(16))) float bias_lds[kBN];
-    __shared__ __attribute__((aligned(16))) float xscale_lds[A8 ? kGroupRows : 1];
+    __shared__ __attribute__((aligned(16))) float xscale_lds[A8 ? kRows : 1];
     const int tid = threadIdx.x, lane = __lane_id(), nw = tid / kWave, lrow = lane % 32, lgrp = lane / 32;
-    const int tiles = tiles_m * tiles_n, tile = blockIdx.x / 2, grp = blockIdx.x % 2;
+    const int tiles = tiles_m * tiles_n, tile = blockIdx.x / (2 * kSJ), grp = blockIdx.x / kSJ % 2, j = blockIdx.x % kSJ;
     const int gsize = group * tiles_m, gi = tile / gsize, gl = tile - gi * gsize, gw = min(group, tiles_n - gi * group);
-    const int n0 = (gi * group + gl % gw) * kCols, m0 = gl / gw * kBM + grp * kGroupRows;
-    const int rows = min(kGroupRows, m - m0);
+    const int n0 = (gi * group + gl % gw) * kCols, m0 = gl / gw * kBM + grp * kGroupRows + j * kRows;
+    const int rows = min(kRows, m - m0);
     if (rows <= 0)
         return;
     using acc_t = std::conditional_t<A8, int, float>;
-    acc_t acc[kSI][kSJ][16];
-    const u32x4_t *src = partial + (int64_t)tile * (kSI * kSJ * 4) * kThreads + grp * kHalf + tid;
+    acc_t acc[kSI][16];
+    const u32x4_t *src = partial + ((int64_t)tile * (kSI * kSJ * 4) + j * 4) * kThreads + grp * kHalf + tid;
     auto add = [&](int s, auto first) {
 #pragma unroll
         for (int i = 0; i < kSI; ++i)
 #pragma unroll
-            for (int j = 0; j < kSJ; ++j)
+            for (int qd = 0; qd < 4; ++qd) {
+                const u32x4_t v = __builtin_nontemporal_load(
+                    src + ((int64_t)s * tiles * (kSI * kSJ * 4) + i * kSJ * 4 + qd) * kThreads);
 #pragma unroll
-                for (int qd = 0; qd < 4; ++qd) {
-                    const u32x4_t v = __builtin_nontemporal_load(
-                        src + ((int64_t)s * tiles * (kSI * kSJ * 4) + (i * kSJ + j) * 4 + qd) * kThreads);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t b = v[e];
-                        const acc_t a = __builtin_bit_cast(acc_t, b);
-                        acc[i][j][4 * qd + e] = decltype(first)::value ? a : acc[i][j][4 * qd + e] + a;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t b = v[e];
+                    const acc_t a = __builtin_bit_cast(acc_t, b);
+                    acc[i][4 * qd + e] = decltype(first)::value ? a : acc[i][4 * qd + e] + a;
                 }
+            }
     };
     add(0, std::true_type{});
     for (int s = 1; s < splits; ++s)
@@ -1542,7 +1543,7 @@ __global__ __launch_bounds__(pp::kThreads / 2) void mfma_join_kernel(const u32x4
         bias_lds[c] = col < n_out && ep.bias ? from16(ep.bias[row], ep.bf16) : 0.0f;
     }
     if constexpr (A8)
-        for (int r = tid; r < kGroupRows; r += kHalf)
+        for (int r = tid; r < kRows; r += kHalf)
             xscale_lds[r] = r < rows ? f16_bits_to_f32(sx[m0 + r]) : 0.0f;
     const bool whole = (n_out % 8) == 0 && n0 + kCols <= n_out;
     if (ep.residual)
@@ -1550,17 +1551,17 @@ __global__ __launch_bounds__(pp::kThreads / 2) void mfma_join_kernel(const u32x4
             *reinterpret_cast<u32x4_t *>(image + c / kPieces * kRow + c % kPieces * 16) =
                 load_row8(ep.residual + (int64_t)(m0 + c / kPieces) * n_out, n0 + c % kPieces * 8, n_out, whole);
     __syncthreads();
-    activate_tile<EPI, kSI, kSJ>(
+    activate_tile<EPI, kSI, 1>(
         ep.activation,
-        [&](int i, int j, int qd, int e) -> float {
+        [&](int i, int, int qd, int e) -> float {
             const int nl = nw * (kSI * 32) + i * 32 + 8 * qd + 4 * lgrp + e;
             if constexpr (A8)
-                return fmaf((float)acc[i][j][4 * qd + e], scale_lds[nl] * xscale_lds[j * 32 + lrow], bias_lds[nl]);
+                return fmaf((float)acc[i][4 * qd + e], scale_lds[nl] * xscale_lds[lrow], bias_lds[nl]);
             else
-                return fmaf(acc[i][j][4 * qd + e], scale_lds[nl], bias_lds[nl]);
+                return fmaf(acc[i][4 * qd + e], scale_lds[nl], bias_lds[nl]);
         },
-        [&](int i, int j, int qd, float (&o)[4]) {
-            put4(image + (j * 32 + lrow) * kRow + tile_channel<EPI>(nw * (kSI * 32) + i * 32 + 8 * qd + 4 * lgrp) * 2, o, ep);
+        [&](int i, int, int qd, float (&o)[4]) {
+            put4(image + lrow * kRow + tile_channel<EPI>(nw * (kSI * 32) + i * 32 + 8 * qd + 4 * lgrp) * 2, o, ep);
         });
     __syncthreads();
     for (int c = tid; c < rows * kPieces; c += kHalf)

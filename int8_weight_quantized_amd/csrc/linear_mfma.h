@@ -63,7 +63,7 @@ hipError_t launch_split(int splits, const LinearArgs &a, void *workspace, hipStr
 {
     const int64_t columns = a.gated ? a.n / 2 : a.n, bn = a.gated ? pp::kBN / 2 : pp::kBN;
     const int64_t tiles_n = (columns + bn - 1) / bn, tiles_m = (a.m + pp::kBM - 1) / pp::kBM, tiles = tiles_m * tiles_n;
-    if (tiles * splits > 0x7fffffff || tiles > 0x3fffffff)
+    if (tiles * splits > 0x7fffffff || tiles > 0x0fffffff)
         return hipErrorInvalidConfiguration;
     const int group = mfma_tile_group(256256, A8, tiles_m, tiles_n);
     u32x4_t *partial = static_cast<u32x4_t *>(workspace);
@@ -79,7 +79,7 @@ hipError_t launch_split(int splits, const LinearArgs &a, void *workspace, hipStr
     if (e != hipSuccess)
         return e;
     auto join = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(2 * tiles)), dim3(pp::kThreads / 2), 0, stream, (const u32x4_t *)partial,
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(2 * pp::kSJ * tiles)), dim3(pp::kThreads / 2), 0, stream, (const u32x4_t *)partial,
                            splits, a.sx, a.scales, a.y, (int)a.m, (int)a.n, (int)tiles_m, (int)tiles_n, group, a.ep);
         return hipGetLastError();
     };
