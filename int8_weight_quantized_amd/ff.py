@@ -379,18 +379,21 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, group
     if need < 0:
         raise ValueError("route_experts does not take these sizes")
     entries = tokens * top_k
-    buf = torch.empty(3 * entries + experts + 1, dtype=torch.int32, device=logits.device)
-    ids, rows, places, offsets = buf.split_with_sizes((entries, entries, entries, experts + 1))
-    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
-    workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    # one allocation: ids, places, weights, rows and offsets, and the workspace
+    # (from 16 bytes on); a call of few tokens is bound by the host
+    rest = -(experts + 1) % 4 + need // 4
+    buf = torch.empty(4 * entries + experts + 1 + rest, dtype=torch.int32, device=logits.device)
     p = buf.data_ptr()
+    places, weights, rows, offsets = p + 4 * entries, p + 8 * entries, p + 12 * entries, p + 16 * entries
+    ws = p + 4 * buf.shape[0] - need
     status = lib.qw_route_experts(
         logits.data_ptr(), code, tokens, experts, top_k, SCORINGS[scoring], _ptr(bias), groups, top_groups,
-        1 if renormalize else 0, scale, p, weights.data_ptr(), p + 12 * entries, p + 4 * entries, p + 8 * entries,
-        workspace.data_ptr(), need, _kv._raw_stream(index))
+        1 if renormalize else 0, scale, p, weights, offsets, rows, places, ws, need, _kv._raw_stream(index))
     if status:
         _raise(status, "qw_route_experts")
-    return ExpertRoute(ids.view(tokens, top_k), weights, offsets, rows, places.view(tokens, top_k))
+    ids, places, weights, rows, offsets, _ = buf.split_with_sizes((entries, entries, entries, entries, experts + 1, rest))
+    shape = (tokens, top_k)
+    return ExpertRoute(ids.view(shape), weights.view(torch.float32).view(shape), offsets, rows, places.view(shape))
 
 
 def _check_route(route):
