@@ -169,11 +169,11 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = F
     except (AttributeError, KeyError, TypeError, ValueError):
         fine = False
     if fine:
-        h = None if residual is None else torch.empty((tokens, k), dtype=dtype, device=x.device)
+        h = None if residual is None else torch.empty(tokens, k, dtype=dtype, device=x.device)
         sh = k
-        made = ((torch.empty((tokens, k), dtype=torch.int8, device=x.device),
+        made = ((torch.empty(tokens, k, dtype=torch.int8, device=x.device),
                  torch.empty(tokens, dtype=torch.float16, device=x.device)) if quantize
-                else (torch.empty((tokens, k), dtype=dtype, device=x.device),))
+                else (torch.empty(tokens, k, dtype=dtype, device=x.device),))
     else:
         device = _pkg._require_gpu(x, "x")
         code, tokens, k, sx, sr, made, h, sh = _validate_norm(x, weight, residual, quantize, out, device)
@@ -258,7 +258,7 @@ def w8a16_linear(x, q, scales, bias=None, activation=None, gated: bool = False, 
     except (AttributeError, TypeError, ValueError, IndexError):
         fine = False
     if fine:
-        y = torch.empty((m, columns), dtype=f16, device=x.device)
+        y = torch.empty(m, columns, dtype=f16, device=x.device)
     else:
         device = _pkg._require_gpu(x, "x")
         m, n, k, y = _validate_linear(x, q, scales, bias, gated, residual, out, f16, device)
@@ -298,7 +298,7 @@ def w8a8_linear(qx, sx, q, scales, bias=None, activation=None, gated: bool = Fal
     except (AttributeError, KeyError, TypeError, ValueError, IndexError):
         fine = False
     if fine:
-        y = torch.empty((m, columns), dtype=dtype, device=qx.device)
+        y = torch.empty(m, columns, dtype=dtype, device=qx.device)
     else:
         device = _pkg._require_gpu(qx, "qx")
         code = _kv._dtype_code(dtype, "dtype")
@@ -454,7 +454,7 @@ def w8a16_experts(x, q, scales, route: ExpertRoute, bias=None, activation=None, 
     except (AttributeError, TypeError, ValueError):
         fine = False
     if fine:
-        y = torch.empty((entries, n // 2 if gated else n), dtype=f16, device=x.device)
+        y = torch.empty(entries, n // 2 if gated else n, dtype=f16, device=x.device)
     else:
         device = _pkg._require_gpu(x, "x")
         x_rows, k, top_k, entries, experts, n, y = _validate_experts(x, q, scales, route, bias, gated, gather, out, device)
@@ -505,7 +505,7 @@ def experts_combine(y, route: ExpertRoute, residual=None, out=None):
     except (AttributeError, TypeError, ValueError):
         fine = False
     if fine:
-        o = torch.empty((tokens, n), dtype=f16, device=y.device)
+        o = torch.empty(tokens, n, dtype=f16, device=y.device)
     else:
         device = _pkg._require_gpu(y, "y")
         tokens, top_k, n, o = _validate_combine(y, route, residual, out, device)
