@@ -149,8 +149,10 @@ __device__ __forceinline__ int best_lane(const Key &k)
     bool top = k.hi == hi && hi != 0;
     uint64_t own = own_lanes<L>(__ballot(top));
     if (TWO && __any((own & (own - 1)) != 0)) {
-        const uint32_t mine = top ? k.lo : 0u;
-        top = top && mine == most_of<L>(mine);
+        // (by all lanes, so not behind `top &&`: moves between lanes read nothing
+        // from lanes that are switched off)
+        const uint32_t mine = top ? k.lo : 0u, lo = most_of<L>(mine);
+        top = top && mine == lo;
         own = own_lanes<L>(__ballot(top));
     }
     return L == 64 ? __ffsll((unsigned long long)own) - 1 : __ffs((uint32_t)own) - 1;
