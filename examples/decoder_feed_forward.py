@@ -67,7 +67,8 @@ class Experts:
         y, h = qw.add_rms_norm(x, self.norm, residual)
         self.route = qw.route_experts(y @ self.router, self.top_k)
         g = qw.w8a16_experts(y, *self.up, self.route, activation="silu", gated=True)
-        return qw.experts_combine(qw.w8a16_experts(g, *self.down, self.route, gather=False), self.route, residual=h)
+        d = qw.w8a16_experts(g, *self.down, self.route, gather=False, dtype=torch.float32)
+        return qw.experts_combine(d, self.route, residual=h)
 
     def reference(self, x, residual):
         """With the route as taken: a token whose choices are close may take

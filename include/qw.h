@@ -1046,6 +1046,19 @@ QW_API qw_status qw_w8a16_experts_path(const uint16_t *x, int64_t x_rows, int ga
                                        int tile, void *stream);
 
 /*
+ * qw_w8a16_experts_f32 -- qw_w8a16_experts_path with y in binary32, [entries][n]
+ * or gated [entries][n / 2]: not rounded, and without binary16's range, for a sum
+ * over the entries that rounds once (qw_experts_combine_f32).  Results are those
+ * of the binary16 call before its rounding.
+ */
+QW_API qw_status qw_w8a16_experts_f32(const uint16_t *x, int64_t x_rows, int gather,
+                                      const int8_t *q, const uint16_t *scales, const uint16_t *bias,
+                                      int activation, int gated, const int32_t *offsets,
+                                      const int32_t *rows, int64_t entries, int64_t top_k, float *y,
+                                      int64_t experts, int64_t n, int64_t k, int path, int tile,
+                                      void *stream);
+
+/*
  * qw_experts_combine -- the sum over each token's experts, in fp32 in the order
  * of j, rounded once:
  *
@@ -1066,6 +1079,10 @@ QW_API qw_status qw_w8a16_experts_path(const uint16_t *x, int64_t x_rows, int ga
 QW_API qw_status qw_experts_combine(const uint16_t *y, int64_t entries, const int32_t *places,
                                     const float *weights, int64_t tokens, int64_t top_k,
                                     const uint16_t *residual, uint16_t *out, int64_t n, void *stream);
+/* The same with y in binary32. */
+QW_API qw_status qw_experts_combine_f32(const float *y, int64_t entries, const int32_t *places,
+                                        const float *weights, int64_t tokens, int64_t top_k,
+                                        const uint16_t *residual, uint16_t *out, int64_t n, void *stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 QW_API const char *qw_status_string(qw_status status);

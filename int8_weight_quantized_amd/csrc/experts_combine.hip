@@ -6,7 +6,7 @@
 // out (and the residual in).  A lane takes 8 columns (16 bytes) of a token and
 // asks for kBatch rows at a time, so that their latencies overlap.  4096 tokens of
 // 2048, 8 experts: 23 us (6.4 TB/s), with a residual 26; 16 tokens 3.4 us; 4096 of
-// 2047, by elements, 82.
+// 2047, by elements, 82.  Rows of fp16 or fp32.
 #include "ff_internal.h"
 #include "kv_device.h"
 
@@ -31,7 +31,44 @@ __device__ __forceinline__ u32x4_t load8(const uint16_t *p, int left)
     return (u32x4_t){w[0], w[1], w[2], w[3]};
 }
 
+// Eight entries' values of a row: as they are loaded, and in fp32.
+template <bool WHOLE, bool F32>
+struct Entries;
 template <bool WHOLE>
+struct Entries<WHOLE, false> {
+    u32x4_t v;
+    __device__ __forceinline__ void load(const void *y, int64_t at, int left)
+    {
+        v = load8<WHOLE>(static_cast<const uint16_t *>(y) + at, left);
+    }
+    __device__ __forceinline__ void values(float (&f)[8]) const { unpack8<QW_F16>(v, f); }
+};
+template <bool WHOLE>
+struct Entries<WHOLE, true> {
+    float v[8];
+    __device__ __forceinline__ void load(const void *y, int64_t at, int left)
+    {
+        const float *p = static_cast<const float *>(y) + at;
+        if (WHOLE) {
+            const float4_t a = *reinterpret_cast<const float4_t *>(p), b = *reinterpret_cast<const float4_t *>(p + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = a[e], v[4 + e] = b[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = e < left ? p[e] : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void values(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = v[e];
+    }
+};
+
+template <bool WHOLE, bool F32>
 __global__ __launch_bounds__(kThreads) void experts_combine_kernel(CombineArgs a, int pieces)
 {
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -46,7 +83,7 @@ __global__ __launch_bounds__(kThreads) void experts_combine_kernel(CombineArgs a
     const int32_t *places = a.places + token * a.top_k;
     const float *weights = a.weights + token * a.top_k;
     for (int j0 = 0; j0 < a.top_k; j0 += kBatch) {
-        u32x4_t v[kBatch];
+        Entries<WHOLE, F32> v[kBatch];
         float w[kBatch];
         bool in[kBatch];
 #pragma unroll
@@ -54,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void experts_combine_kernel(CombineArgs a
             const int32_t p = j0 + b < a.top_k ? places[j0 + b] : -1;
             in[b] = p >= 0 && p < a.entries;
             if (in[b]) {
-                v[b] = load8<WHOLE>(a.y + p * a.n + c, left);
+                v[b].load(a.y, p * a.n + c, left);
                 w[b] = weights[j0 + b];
             }
         }
@@ -62,7 +99,7 @@ __global__ __launch_bounds__(kThreads) void experts_combine_kernel(CombineArgs a
         for (int b = 0; b < kBatch; ++b)
             if (in[b]) {
                 float f[8];
-                unpack8<QW_F16>(v[b], f);
+                v[b].values(f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     sum[e] = fmaf(w[b], f[e], sum[e]);
@@ -87,11 +124,13 @@ hipError_t launch_experts_combine(const CombineArgs &a, hipStream_t stream)
     const int64_t blocks = (a.tokens * pieces + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    if (a.n % 8 == 0)
-        experts_combine_kernel<true><<<dim3((unsigned)blocks), dim3(kThreads), 0, stream>>>(a, (int)pieces);
-    else
-        experts_combine_kernel<false><<<dim3((unsigned)blocks), dim3(kThreads), 0, stream>>>(a, (int)pieces);
-    return hipGetLastError();
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, (int)pieces);
+        return hipGetLastError();
+    };
+    if (a.f32)
+        return a.n % 8 == 0 ? launch(experts_combine_kernel<true, true>) : launch(experts_combine_kernel<false, true>);
+    return a.n % 8 == 0 ? launch(experts_combine_kernel<true, false>) : launch(experts_combine_kernel<false, false>);
 }
 
 } // namespace qw

@@ -270,6 +270,67 @@ int64_t route_blocks(int64_t tokens)
 
 int64_t route_workspace(int64_t tokens, int64_t experts) { return route_blocks(tokens) * ((experts + 3) / 4) * 16; }
 
+qw_status experts_product(const uint16_t *x, int64_t x_rows, int gather, const int8_t *q, const uint16_t *scales,
+                          const uint16_t *bias, int activation, int gated, const int32_t *offsets, const int32_t *rows,
+                          int64_t entries, int64_t top_k, void *y, bool f32, int64_t experts, int64_t n, int64_t k, int path,
+                          int tile, void *stream)
+{
+    if ((path != QW_PATH_AUTO && path != QW_PATH_SKINNY && path != QW_PATH_MFMA) ||
+        (tile != 0 && (path != QW_PATH_MFMA || !known_tile(tile, false) || tile == 128128)))
+        return QW_ERROR_INVALID_VALUE;
+    if (x_rows < 0 || entries < 0 || n < 0 || k <= 0 || experts < 1 || top_k < 1 || (gather != 0 && gather != 1) ||
+        (!gather && x_rows != entries) || (gated != 0 && gated != 1) || (gated && n % 2) || activation < QW_ACT_NONE ||
+        activation > QW_ACT_SILU)
+        return QW_ERROR_INVALID_VALUE;
+    if (entries == 0 || n == 0)
+        return QW_SUCCESS;
+    if ((!x && x_rows > 0) || !q || !scales || !offsets || (gather && !rows) || !y)
+        return QW_ERROR_INVALID_VALUE;
+    if (k % 16 != 0 || experts > QW_MAX_EXPERTS || entries > kMaxDim || x_rows > kMaxDim || n > kMaxDim || top_k > kMaxDim ||
+        k > QW_MFMA_MAX_K || n * k >= int64_t(1) << 32 || (gather && (x_rows + 1) * k >= int64_t(1) << 31) ||
+        (path == QW_PATH_SKINNY && entries > (1 << 19)) || (tile == 256256 && k > qw::kPingPongMaxK))
+        return QW_ERROR_UNSUPPORTED;
+    if (off16(x) || off16(q) || off16(scales) || off16(bias) || off16(y) || off4(offsets) || off4(rows))
+        return QW_ERROR_MISALIGNED;
+    const uint64_t E = (uint64_t)experts, un = (uint64_t)n, uk = (uint64_t)k;
+    const Span out = {y, (uint64_t)entries * (gated ? un / 2 : un) * (f32 ? 4u : 2u)};
+    if (meet(out, {x, (uint64_t)x_rows * uk * 2u}) || meet(out, {q, E * un * uk}) || meet(out, {scales, E * un * 2u}) ||
+        meet(out, {bias, E * un * 2u}) || meet(out, {offsets, (E + 1) * 4u}) || meet(out, {rows, (uint64_t)entries * 4u}))
+        return QW_ERROR_INVALID_VALUE;
+    const qw::LinearArgs a = {x, nullptr, q, scales, {bias, nullptr, activation, 0}, gated != 0, static_cast<uint16_t *>(y), entries, n, k};
+    const qw::Experts ex = {offsets, gather ? rows : nullptr, (int)experts, (int)entries, (int)x_rows, (int)top_k};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (path == QW_PATH_AUTO)
+        path = entries <= 12 * experts && entries <= (1 << 19) ? QW_PATH_SKINNY : QW_PATH_MFMA;
+    if (path == QW_PATH_SKINNY)
+        return status_of(qw::launch_skinny_experts(a, ex, f32, s));
+    if (tile == 0)
+        tile = experts_tile(entries / experts, k);
+    return status_of(qw::launch_mfma_experts(tile, a, ex, f32, s));
+}
+
+qw_status combine(const void *y, bool f32, int64_t entries, const int32_t *places, const float *weights, int64_t tokens,
+                  int64_t top_k, const uint16_t *residual, uint16_t *out, int64_t n, void *stream)
+{
+    if (entries < 0 || tokens < 0 || top_k < 1 || n < 0)
+        return QW_ERROR_INVALID_VALUE;
+    if (tokens == 0 || n == 0)
+        return QW_SUCCESS;
+    if ((!y && entries > 0) || !places || !weights || !out)
+        return QW_ERROR_INVALID_VALUE;
+    if (entries > kMaxDim || tokens > kMaxDim || top_k > kMaxDim || n > kMaxDim || tokens > (int64_t(1) << 40) / n)
+        return QW_ERROR_UNSUPPORTED;
+    if (off16(y) || off16(residual) || off16(out) || off4(places) || off4(weights))
+        return QW_ERROR_MISALIGNED;
+    const uint64_t t = (uint64_t)tokens, un = (uint64_t)n;
+    const Span to = {out, t * un * 2u};
+    if (meet(to, {y, (uint64_t)entries * un * (f32 ? 4u : 2u)}) || meet(to, {places, t * (uint64_t)top_k * 4u}) ||
+        meet(to, {weights, t * (uint64_t)top_k * 4u}) || (residual != out && meet(to, {residual, t * un * 2u})))
+        return QW_ERROR_INVALID_VALUE;
+    const qw::CombineArgs a = {y, places, weights, residual, out, tokens, entries, n, (int)top_k, f32};
+    return status_of(qw::launch_experts_combine(a, static_cast<hipStream_t>(stream)));
+}
+
 } // namespace
 
 extern "C" {
@@ -376,38 +437,17 @@ QW_API qw_status qw_w8a16_experts_path(const uint16_t *x, int64_t x_rows, int ga
                                        const int32_t *rows, int64_t entries, int64_t top_k, uint16_t *y, int64_t experts,
                                        int64_t n, int64_t k, int path, int tile, void *stream)
 {
-    if ((path != QW_PATH_AUTO && path != QW_PATH_SKINNY && path != QW_PATH_MFMA) ||
-        (tile != 0 && (path != QW_PATH_MFMA || !known_tile(tile, false) || tile == 128128)))
-        return QW_ERROR_INVALID_VALUE;
-    if (x_rows < 0 || entries < 0 || n < 0 || k <= 0 || experts < 1 || top_k < 1 || (gather != 0 && gather != 1) ||
-        (!gather && x_rows != entries) || (gated != 0 && gated != 1) || (gated && n % 2) || activation < QW_ACT_NONE ||
-        activation > QW_ACT_SILU)
-        return QW_ERROR_INVALID_VALUE;
-    if (entries == 0 || n == 0)
-        return QW_SUCCESS;
-    if ((!x && x_rows > 0) || !q || !scales || !offsets || (gather && !rows) || !y)
-        return QW_ERROR_INVALID_VALUE;
-    if (k % 16 != 0 || experts > QW_MAX_EXPERTS || entries > kMaxDim || x_rows > kMaxDim || n > kMaxDim || top_k > kMaxDim ||
-        k > QW_MFMA_MAX_K || n * k >= int64_t(1) << 32 || (gather && (x_rows + 1) * k >= int64_t(1) << 31) ||
-        (path == QW_PATH_SKINNY && entries > (1 << 19)) || (tile == 256256 && k > qw::kPingPongMaxK))
-        return QW_ERROR_UNSUPPORTED;
-    if (off16(x) || off16(q) || off16(scales) || off16(bias) || off16(y) || off4(offsets) || off4(rows))
-        return QW_ERROR_MISALIGNED;
-    const uint64_t E = (uint64_t)experts, un = (uint64_t)n, uk = (uint64_t)k;
-    const Span out = {y, (uint64_t)entries * (gated ? un / 2 : un) * 2u};
-    if (meet(out, {x, (uint64_t)x_rows * uk * 2u}) || meet(out, {q, E * un * uk}) || meet(out, {scales, E * un * 2u}) ||
-        meet(out, {bias, E * un * 2u}) || meet(out, {offsets, (E + 1) * 4u}) || meet(out, {rows, (uint64_t)entries * 4u}))
-        return QW_ERROR_INVALID_VALUE;
-    const qw::LinearArgs a = {x, nullptr, q, scales, {bias, nullptr, activation, 0}, gated != 0, y, entries, n, k};
-    const qw::Experts ex = {offsets, gather ? rows : nullptr, (int)experts, (int)entries, (int)x_rows, (int)top_k};
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    if (path == QW_PATH_AUTO)
-        path = entries <= 12 * experts && entries <= (1 << 19) ? QW_PATH_SKINNY : QW_PATH_MFMA;
-    if (path == QW_PATH_SKINNY)
-        return status_of(qw::launch_skinny_experts(a, ex, s));
-    if (tile == 0)
-        tile = experts_tile(entries / experts, k);
-    return status_of(qw::launch_mfma_experts(tile, a, ex, s));
+    return experts_product(x, x_rows, gather, q, scales, bias, activation, gated, offsets, rows, entries, top_k, y, false, experts,
+                           n, k, path, tile, stream);
+}
+
+QW_API qw_status qw_w8a16_experts_f32(const uint16_t *x, int64_t x_rows, int gather, const int8_t *q, const uint16_t *scales,
+                                      const uint16_t *bias, int activation, int gated, const int32_t *offsets,
+                                      const int32_t *rows, int64_t entries, int64_t top_k, float *y, int64_t experts, int64_t n,
+                                      int64_t k, int path, int tile, void *stream)
+{
+    return experts_product(x, x_rows, gather, q, scales, bias, activation, gated, offsets, rows, entries, top_k, y, true, experts,
+                           n, k, path, tile, stream);
 }
 
 QW_API qw_status qw_w8a16_experts(const uint16_t *x, int64_t x_rows, int gather, const int8_t *q, const uint16_t *scales,
@@ -423,23 +463,14 @@ QW_API qw_status qw_experts_combine(const uint16_t *y, int64_t entries, const in
                                     int64_t tokens, int64_t top_k, const uint16_t *residual, uint16_t *out, int64_t n,
                                     void *stream)
 {
-    if (entries < 0 || tokens < 0 || top_k < 1 || n < 0)
-        return QW_ERROR_INVALID_VALUE;
-    if (tokens == 0 || n == 0)
-        return QW_SUCCESS;
-    if ((!y && entries > 0) || !places || !weights || !out)
-        return QW_ERROR_INVALID_VALUE;
-    if (entries > kMaxDim || tokens > kMaxDim || top_k > kMaxDim || n > kMaxDim || tokens > (int64_t(1) << 40) / n)
-        return QW_ERROR_UNSUPPORTED;
-    if (off16(y) || off16(residual) || off16(out) || off4(places) || off4(weights))
-        return QW_ERROR_MISALIGNED;
-    const uint64_t t = (uint64_t)tokens, un = (uint64_t)n;
-    const Span to = {out, t * un * 2u};
-    if (meet(to, {y, (uint64_t)entries * un * 2u}) || meet(to, {places, t * (uint64_t)top_k * 4u}) ||
-        meet(to, {weights, t * (uint64_t)top_k * 4u}) || (residual != out && meet(to, {residual, t * un * 2u})))
-        return QW_ERROR_INVALID_VALUE;
-    const qw::CombineArgs a = {y, places, weights, residual, out, tokens, entries, n, (int)top_k};
-    return status_of(qw::launch_experts_combine(a, static_cast<hipStream_t>(stream)));
+    return combine(y, false, entries, places, weights, tokens, top_k, residual, out, n, stream);
+}
+
+QW_API qw_status qw_experts_combine_f32(const float *y, int64_t entries, const int32_t *places, const float *weights,
+                                        int64_t tokens, int64_t top_k, const uint16_t *residual, uint16_t *out, int64_t n,
+                                        void *stream)
+{
+    return combine(y, true, entries, places, weights, tokens, top_k, residual, out, n, stream);
 }
 
 QW_API int64_t qw_w8a16_linear_workspace(int64_t m, int64_t n, int64_t k, int gated)

@@ -39,13 +39,14 @@ int64_t route_tokens_a_block(int64_t tokens);
 hipError_t launch_route_experts(const RouteArgs &a, int dtype, hipStream_t stream);
 
 struct CombineArgs {
-    const uint16_t *y;       // fp16 [entries][n]
+    const void *y;           // fp16 or, `f32`, fp32 [entries][n]
     const int32_t *places;   // [tokens][top_k]
     const float *weights;    // [tokens][top_k]
     const uint16_t *residual; // fp16 [tokens][n], or null
     uint16_t *out;           // fp16 [tokens][n]
     int64_t tokens, entries, n;
     int top_k;
+    bool f32;
 };
 hipError_t launch_experts_combine(const CombineArgs &a, hipStream_t stream);
 

@@ -115,6 +115,8 @@ __device__ __forceinline__ int xcd_remap(int bid, int nblocks)
 // The activation is branched on once, by class, around the unrolled code.  A
 // residual is staged through the output image in LDS, coalesced, and added
 // there by the lane that holds the output: one rounding.
+//
+// F32: a grouped product's outputs stay in fp32, stored from the registers.
 // ---------------------------------------------------------------------------
 
 constexpr bool is_gated(int epi) { return epi == kGated || epi == kPartialGated; }
@@ -225,9 +227,24 @@ __device__ __forceinline__ uint32_t entry_offset(const Experts &ex, int p, int m
     return (uint32_t)(row < 0 ? ex.x_rows : row) * (uint32_t)k * 2u;
 }
 
+// Four outputs of a row of fp32 from column c: rows of their own lines, so that
+// the caches put the pieces together (four of them are 128 bytes), without an
+// image in LDS, for which the tile is twice too large.
+__device__ __forceinline__ void put4_f32(float *row, int c, int n_out, const float (&o)[4])
+{
+    if (n_out % 4 == 0 && c + 4 <= n_out) {
+        *reinterpret_cast<float4v *>(row + c) = (float4v){o[0], o[1], o[2], o[3]};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (c + e < n_out)
+            row[c + e] = o[e];
+}
+
 // A grouped product's tile of entries of no expert: rows [m0, m1) of zeros.
-template <int COLS, int THREADS>
-__device__ __forceinline__ void zero_rows(uint16_t *y, int m0, int m1, int n0, int n_out)
+template <int COLS, int THREADS, class T>
+__device__ __forceinline__ void zero_rows(T *y, int m0, int m1, int n0, int n_out)
 {
     for (int64_t e = threadIdx.x; e < (int64_t)(m1 - m0) * COLS; e += THREADS) {
         const int c = n0 + (int)(e % COLS);
@@ -308,7 +325,7 @@ using stage_t = std::integral_constant<int, I>;
 // the epilogue multiplies by S[n] * Sx[m].  Otherwise x is fp16 and sx is
 // unused.  OL: exact outlier side lists (at most kMfmaOutlierSlots per
 // weight row) are added to the accumulators after the main loop.
-template <int NW, int BN, int BM, bool A8, bool OL = false, bool ZP = false, int EPI = kPlain, bool GRP = false>
+template <int NW, int BN, int BM, bool A8, bool OL = false, bool ZP = false, int EPI = kPlain, bool GRP = false, bool F32 = false>
 __global__ __launch_bounds__(NW * 64)
 __attribute__((amdgpu_waves_per_eu(NW == 4 && BM > 128 ? 1 : 2))) void mfma_gemm_dma_kernel(
     const void *__restrict__ xv, const uint16_t *__restrict__ sx, const int8_t *__restrict__ q,
@@ -317,6 +334,8 @@ __attribute__((amdgpu_waves_per_eu(NW == 4 && BM > 128 ? 1 : 2))) void mfma_gemm
 {
     static_assert(EPI == kPlain || (!OL && !ZP), "an epilogue goes with symmetric codes");
     static_assert(!GRP || (EPI != kPlain && !A8), "grouped products are W8A16 with an epilogue");
+    static_assert(GRP || !F32, "fp32 outputs: grouped products");
+    using out_t = std::conditional_t<F32, float, uint16_t>;
     using C = DmaCfg<NW, BN, BM, A8>;
     constexpr int kCols = EPI == kGated ? BN / 2 : BN; // columns of Y a tile
     const int n_out = EPI == kGated ? n / 2 : n;
@@ -362,7 +381,7 @@ __attribute__((amdgpu_waves_per_eu(NW == 4 && BM > 128 ? 1 : 2))) void mfma_gemm
         m0 = rows.begin;
         m = rows.end;
         if (rows.expert == ex.count) {
-            zero_rows<kCols, C::kThreads>(y, m0, min(m, m0 + BM), n0, n_out);
+            zero_rows<kCols, C::kThreads>(reinterpret_cast<out_t *>(y), m0, min(m, m0 + BM), n0, n_out);
             return;
         }
         q += (int64_t)rows.expert * n * k;
@@ -796,8 +815,16 @@ __attribute__((amdgpu_waves_per_eu(NW == 4 && BM > 128 ? 1 : 2))) void mfma_gemm
                     return fmaf(acc[i][j][4 * qd + e], scale_lds[nl], bias_lds[nl]);
             },
             [&](int i, int j, int qd, float (&o)[4]) {
-                put4(image(j * 32 + lrow) + tile_channel<EPI>(wave * C::kWaveN + i * 32 + 8 * qd + 4 * lgrp) * 2, o, ep);
+                const int row = j * 32 + lrow, c = tile_channel<EPI>(wave * C::kWaveN + i * 32 + 8 * qd + 4 * lgrp);
+                if constexpr (F32) {
+                    if (row < rows)
+                        put4_f32(reinterpret_cast<float *>(y) + (int64_t)(m0 + row) * n_out, n0 + c, n_out, o);
+                } else {
+                    put4(image(row) + c * 2, o, ep);
+                }
             });
+        if constexpr (F32)
+            return;
         ring_barrier();
         for (int c = tid; c < rows * kPieces; c += C::kThreads)
             store_row8(y + (int64_t)(m0 + c / kPieces) * n_out, n0 + c % kPieces * 8, n_out, whole,
@@ -932,7 +959,7 @@ static_assert(pp::kBM * kPingPongMaxK * 2 <= (int64_t(1) << 31), "buffer range")
 // EPI kPartial, kPartialGated: the grid holds `splits` copies of the tiles, of which copy s
 // multiplies the k steps from s / splits of them on and leaves its accumulators
 // in `partial`, [copy][tile][quad of registers][thread], for mfma_join_kernel.
-template <bool A8, bool OL, bool ZP, int EPI = kPlain, bool GRP = false>
+template <bool A8, bool OL, bool ZP, int EPI = kPlain, bool GRP = false, bool F32 = false>
 __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
     const void *__restrict__ xv, const uint16_t *__restrict__ sx, const int8_t *__restrict__ q,
     const uint16_t *__restrict__ scales, const int8_t *__restrict__ zeros, OutlierList ol,
@@ -941,6 +968,8 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
 {
     static_assert(EPI == kPlain || (!OL && !ZP), "an epilogue goes with symmetric codes");
     static_assert(!GRP || (EPI != kPlain && !A8), "grouped products are W8A16 with an epilogue");
+    static_assert(GRP || !F32, "fp32 outputs: grouped products");
+    using out_t = std::conditional_t<F32, float, uint16_t>;
     using namespace pp;
     constexpr int kCols = is_gated(EPI) ? kBN / 2 : kBN; // columns of Y a tile
     const int n_out = is_gated(EPI) ? n / 2 : n;
@@ -993,7 +1022,7 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
         m0 = rows.begin;
         m = rows.end;
         if (rows.expert == ex.count) {
-            zero_rows<kCols, kThreads>(y, m0, min(m, m0 + kBM), n0, n_out);
+            zero_rows<kCols, kThreads>(reinterpret_cast<out_t *>(y), m0, min(m, m0 + kBM), n0, n_out);
             return;
         }
         q += (int64_t)rows.expert * n * k;
@@ -1358,9 +1387,16 @@ __global__ __launch_bounds__(pp::kThreads) void mfma_pp_kernel(
                     return fmaf(acc[i][j][4 * qd + e], scale_lds[nl], bias_lds[nl]);
             },
             [&](int i, int j, int qd, float (&o)[4]) {
-                put4(image(grp * kGroupRows + j * 32 + lrow) + tile_channel<EPI>(nw * (kSI * 32) + i * 32 + 8 * qd + 4 * lgrp) * 2,
-                     o, ep);
+                const int row = grp * kGroupRows + j * 32 + lrow, c = tile_channel<EPI>(nw * (kSI * 32) + i * 32 + 8 * qd + 4 * lgrp);
+                if constexpr (F32) {
+                    if (row < rows)
+                        put4_f32(reinterpret_cast<float *>(y) + (int64_t)(m0 + row) * n_out, n0 + c, n_out, o);
+                } else {
+                    put4(image(row) + c * 2, o, ep);
+                }
             });
+        if constexpr (F32)
+            return;
         ring_barrier();
         for (int c = tid; c < rows * kPieces; c += kThreads)
             store_row8(y + (int64_t)(m0 + c / kPieces) * n_out, n0 + c % kPieces * 8, n_out, whole,

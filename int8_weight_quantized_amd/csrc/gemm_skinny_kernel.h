@@ -74,9 +74,11 @@ constexpr int kSkinnyTargetWaves = 2048; // enough in-flight loads to fill HBM
 // PART (with RW > 1): the reduction split over `parts` workgroups too (blockIdx.z).
 // kParts leaves each one's sums in `partial`, and kJoin, a launch of its own with
 // the same RT, MT and RW, adds them in the parts' order for the epilogue.
+//
+// F32: a grouped product's outputs stay in fp32.
 enum { kWhole = 0, kParts = 1, kJoin = 2 };
 template <int RT, int MT, int KSPLIT, bool A8 = false, bool ZP = false, int EPI = kPlain, bool GRP = false, int RW = 1,
-          int PART = kWhole>
+          int PART = kWhole, bool F32 = false>
 __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
     const void *__restrict__ xv, const uint16_t *__restrict__ sx, const int8_t *__restrict__ q,
     const uint16_t *__restrict__ scales, const int8_t *__restrict__ zeros, OutlierList ol,
@@ -85,6 +87,7 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
     static_assert(EPI == kPlain || !ZP, "symmetric codes");
     static_assert(EPI != kGated || RT % 2 == 0, "gate and up in pairs of tiles");
     static_assert(!GRP || (EPI != kPlain && !A8), "grouped products are W8A16 with an epilogue");
+    static_assert(GRP || !F32, "fp32 outputs: grouped products");
     static_assert(RW == 1 || (EPI != kPlain && !GRP), "shared activations: products with an epilogue");
     static_assert(PART == kWhole || (RW > 1 && (PART == kParts || KSPLIT == 1)), "parts of wide workgroups");
     const uint16_t *__restrict__ x = static_cast<const uint16_t *>(xv);
@@ -124,7 +127,8 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
         if (tile.expert == ex.count) { // entries of no expert: rows of zeros
             for (int e = threadIdx.x; e < 16 * MT * kCols; e += KSPLIT * kWave)
                 if (m0 + e / kCols < m && n0 + e % kCols < n_out)
-                    y[(int64_t)(m0 + e / kCols) * n_out + n0 + e % kCols] = 0;
+                    reinterpret_cast<std::conditional_t<F32, float, uint16_t> *>(y)[(int64_t)(m0 + e / kCols) * n_out + n0 +
+                                                                                    e % kCols] = 0;
             return;
         }
         q += (int64_t)tile.expert * n * k;
@@ -532,6 +536,18 @@ __global__ __launch_bounds__(RW * KSPLIT * 64) void skinny_gemm_kernel(
                 for (int j = 0; j < 8; ++j)
                     if (n0 + 8 * pc + j < n)
                         dst[j] = ytile[row][8 * pc + j];
+            }
+        } else if constexpr (F32) {
+            float *to = reinterpret_cast<float *>(y) + (int64_t)ym * n_out + n0 + 8 * pc;
+            const float *from = &ytile[row][8 * pc];
+            if (vec_ok) {
+                *reinterpret_cast<float4v *>(to) = *reinterpret_cast<const float4v *>(from);
+                *reinterpret_cast<float4v *>(to + 4) = *reinterpret_cast<const float4v *>(from + 4);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (n0 + 8 * pc + j < n_out)
+                        to[j] = from[j];
             }
         } else {
             const uint16_t *res = ep.residual ? ep.residual + (int64_t)ym * n_out + n0 + 8 * pc : nullptr;

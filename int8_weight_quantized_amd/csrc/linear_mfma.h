@@ -7,7 +7,7 @@
 namespace qw {
 namespace {
 
-template <int NW, int BN, int BM, bool A8, bool GRP>
+template <int NW, int BN, int BM, bool A8, bool GRP, bool F32>
 hipError_t launch_linear_tile(int tile, const LinearArgs &a, const Experts &ex, hipStream_t stream)
 {
     constexpr bool kPp = BN == 256 && BM == 256;
@@ -29,29 +29,29 @@ hipError_t launch_linear_tile(int tile, const LinearArgs &a, const Experts &ex, 
         return hipGetLastError();
     };
     if constexpr (kPp)
-        return a.gated ? launch(mfma_pp_kernel<A8, false, false, kGated, GRP>, pp::kThreads, 1, (u32x4_t *)nullptr)
-                       : launch(mfma_pp_kernel<A8, false, false, kLinear, GRP>, pp::kThreads, 1, (u32x4_t *)nullptr);
+        return a.gated ? launch(mfma_pp_kernel<A8, false, false, kGated, GRP, F32>, pp::kThreads, 1, (u32x4_t *)nullptr)
+                       : launch(mfma_pp_kernel<A8, false, false, kLinear, GRP, F32>, pp::kThreads, 1, (u32x4_t *)nullptr);
     else
-        return a.gated ? launch(mfma_gemm_dma_kernel<NW, BN, BM, A8, false, false, kGated, GRP>, NW * kWave)
-                       : launch(mfma_gemm_dma_kernel<NW, BN, BM, A8, false, false, kLinear, GRP>, NW * kWave);
+        return a.gated ? launch(mfma_gemm_dma_kernel<NW, BN, BM, A8, false, false, kGated, GRP, F32>, NW * kWave)
+                       : launch(mfma_gemm_dma_kernel<NW, BN, BM, A8, false, false, kLinear, GRP, F32>, NW * kWave);
 }
 
-template <bool A8, bool GRP>
+template <bool A8, bool GRP, bool F32 = false>
 hipError_t launch_linear_tiles(int tile, const LinearArgs &a, const Experts &ex, hipStream_t stream)
 {
     switch (tile) {
     case 256256:
-        return launch_linear_tile<8, 256, 256, A8, GRP>(tile, a, ex, stream);
+        return launch_linear_tile<8, 256, 256, A8, GRP, F32>(tile, a, ex, stream);
     case 256128:
-        return launch_linear_tile<4, 256, 128, A8, GRP>(tile, a, ex, stream);
+        return launch_linear_tile<4, 256, 128, A8, GRP, F32>(tile, a, ex, stream);
     case 256064:
-        return launch_linear_tile<4, 256, 64, A8, GRP>(tile, a, ex, stream);
+        return launch_linear_tile<4, 256, 64, A8, GRP, F32>(tile, a, ex, stream);
     case 128128:
         if constexpr (!A8 && !GRP)
-            return launch_linear_tile<4, 128, 128, A8, GRP>(tile, a, ex, stream);
+            return launch_linear_tile<4, 128, 128, A8, GRP, F32>(tile, a, ex, stream);
         return hipErrorInvalidValue;
     case 128064:
-        return launch_linear_tile<4, 128, 64, A8, GRP>(tile, a, ex, stream);
+        return launch_linear_tile<4, 128, 64, A8, GRP, F32>(tile, a, ex, stream);
     default:
         return hipErrorInvalidValue;
     }

@@ -5,7 +5,7 @@
 namespace qw {
 namespace {
 
-template <int RT, int MT, int KSPLIT, bool A8, int EPI, bool GRP, int RW = 1, int PART = kWhole>
+template <int RT, int MT, int KSPLIT, bool A8, int EPI, bool GRP, int RW = 1, int PART = kWhole, bool F32 = false>
 hipError_t launch_cfg(const LinearArgs &a, const Experts &ex, hipStream_t stream, void *sums = nullptr, int parts = 1)
 {
     constexpr int kCols = RW * (EPI == kGated ? 8 * RT : 16 * RT);
@@ -15,7 +15,7 @@ hipError_t launch_cfg(const LinearArgs &a, const Experts &ex, hipStream_t stream
     if (tiles_m > 65535)
         return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)tiles_n, (unsigned)tiles_m, PART == kParts ? (unsigned)parts : 1u);
-    hipLaunchKernelGGL((skinny_gemm_kernel<RT, MT, KSPLIT, A8, false, EPI, GRP, RW, PART>), grid, dim3(RW * KSPLIT * kWave), 0,
+    hipLaunchKernelGGL((skinny_gemm_kernel<RT, MT, KSPLIT, A8, false, EPI, GRP, RW, PART, F32>), grid, dim3(RW * KSPLIT * kWave), 0,
                        stream, a.x, a.sx, a.q, a.scales, (const int8_t *)nullptr, OutlierList{nullptr, nullptr, 0}, a.y, (int)a.m,
                        (int)a.n, (int)a.k, a.ep, ex, sums, parts);
     return hipGetLastError();
@@ -23,7 +23,7 @@ hipError_t launch_cfg(const LinearArgs &a, const Experts &ex, hipStream_t stream
 
 // As for the plain products: k is split until the grid holds about
 // kSkinnyTargetWaves waves, within the largest split of each variant.
-template <int RT, int MT, bool A8, int EPI, bool GRP>
+template <int RT, int MT, bool A8, int EPI, bool GRP, bool F32 = false>
 hipError_t launch_split(const LinearArgs &a, const Experts &ex, int64_t row_tiles, hipStream_t stream)
 {
     constexpr int kMaxSplit = RT == 4 ? 4 : (A8 || MT > 1 || GRP) ? 8 : 16;
@@ -34,18 +34,18 @@ hipError_t launch_split(const LinearArgs &a, const Experts &ex, int64_t row_tile
         ksplit *= 2;
     switch (ksplit) {
     case 1:
-        return launch_cfg<RT, MT, 1, A8, EPI, GRP>(a, ex, stream);
+        return launch_cfg<RT, MT, 1, A8, EPI, GRP, 1, kWhole, F32>(a, ex, stream);
     case 2:
-        return launch_cfg<RT, MT, 2, A8, EPI, GRP>(a, ex, stream);
+        return launch_cfg<RT, MT, 2, A8, EPI, GRP, 1, kWhole, F32>(a, ex, stream);
     case 4:
-        return launch_cfg<RT, MT, 4, A8, EPI, GRP>(a, ex, stream);
+        return launch_cfg<RT, MT, 4, A8, EPI, GRP, 1, kWhole, F32>(a, ex, stream);
     case 8:
         if constexpr (kMaxSplit >= 8)
-            return launch_cfg<RT, MT, 8, A8, EPI, GRP>(a, ex, stream);
+            return launch_cfg<RT, MT, 8, A8, EPI, GRP, 1, kWhole, F32>(a, ex, stream);
         break;
     default:
         if constexpr (kMaxSplit >= 16)
-            return launch_cfg<RT, MT, 16, A8, EPI, GRP>(a, ex, stream);
+            return launch_cfg<RT, MT, 16, A8, EPI, GRP, 1, kWhole, F32>(a, ex, stream);
         break;
     }
     return hipErrorInvalidValue; // not reached: ksplit <= kMaxSplit
@@ -149,9 +149,12 @@ hipError_t launch_skinny_linear(const LinearArgs &a, hipStream_t stream)
     return a.gated ? launch_rows<false, kGated>(a, stream) : launch_rows<false, kLinear>(a, stream);
 }
 
-hipError_t launch_skinny_experts(const LinearArgs &a, const Experts &ex, hipStream_t stream)
+hipError_t launch_skinny_experts(const LinearArgs &a, const Experts &ex, bool f32, hipStream_t stream)
 {
     const int64_t row_tiles = a.m < ex.count ? a.m : ex.count; // (about as many have rows)
+    if (f32)
+        return a.gated ? launch_split<2, 1, false, kGated, true, true>(a, ex, row_tiles, stream)
+                       : launch_split<2, 1, false, kLinear, true, true>(a, ex, row_tiles, stream);
     return a.gated ? launch_split<2, 1, false, kGated, true>(a, ex, row_tiles, stream)
                    : launch_split<2, 1, false, kLinear, true>(a, ex, row_tiles, stream);
 }

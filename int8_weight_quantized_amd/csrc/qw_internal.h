@@ -195,8 +195,8 @@ hipError_t launch_mfma_linear_a8(int tile, const LinearArgs &a, hipStream_t stre
 int64_t mfma_split_bytes(int64_t m, int64_t n, int splits);
 hipError_t launch_mfma_split(int splits, const LinearArgs &a, void *workspace, hipStream_t stream);
 hipError_t launch_mfma_split_a8(int splits, const LinearArgs &a, void *workspace, hipStream_t stream);
-// Grouped: a.m entries.
-hipError_t launch_skinny_experts(const LinearArgs &a, const Experts &ex, hipStream_t stream);
-hipError_t launch_mfma_experts(int tile, const LinearArgs &a, const Experts &ex, hipStream_t stream);
+// Grouped: a.m entries.  f32: a.y is of fp32.
+hipError_t launch_skinny_experts(const LinearArgs &a, const Experts &ex, bool f32, hipStream_t stream);
+hipError_t launch_mfma_experts(int tile, const LinearArgs &a, const Experts &ex, bool f32, hipStream_t stream);
 
 } // namespace qw

@@ -11,7 +11,8 @@ and with experts instead of one product for all tokens
     y, h = add_rms_norm(x, weight, residual=h)
     route = route_experts(y @ router.T, top_k)
     g = w8a16_experts(y, *gate_up, route, activation="silu", gated=True)
-    x = experts_combine(w8a16_experts(g, *down, route, gather=False), route, residual=h)
+    d = w8a16_experts(g, *down, route, gather=False, dtype=torch.float32)
+    x = experts_combine(d, route, residual=h)
 
 As everywhere in this package, the calls check their arguments, allocate
 outputs with torch and enqueue HIP kernels on the current stream; none of them
@@ -61,10 +62,11 @@ def _declare(lib):
     experts = [vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, i64, i64, vp, i64, i64, i64]
     lib.qw_w8a16_experts.argtypes = experts + [vp]
     lib.qw_w8a16_experts_path.argtypes = experts + [i32, i32, vp]
-    lib.qw_experts_combine.argtypes = [vp, i64, vp, vp, i64, i64, vp, vp, i64, vp]
+    lib.qw_w8a16_experts_f32.argtypes = experts + [i32, i32, vp]
+    lib.qw_experts_combine.argtypes = lib.qw_experts_combine_f32.argtypes = [vp, i64, vp, vp, i64, i64, vp, vp, i64, vp]
     for f in (lib.qw_add_rms_norm, lib.qw_add_rms_norm_quantize, lib.qw_w8a16_linear, lib.qw_w8a16_linear_path,
               lib.qw_w8a8_linear, lib.qw_w8a8_linear_path, lib.qw_route_experts, lib.qw_w8a16_experts,
-              lib.qw_w8a16_experts_path, lib.qw_experts_combine):
+              lib.qw_w8a16_experts_path, lib.qw_w8a16_experts_f32, lib.qw_experts_combine, lib.qw_experts_combine_f32):
         f.restype = i32
     lib.qw_route_experts_workspace.restype = i64
 
@@ -401,9 +403,13 @@ def _check_route(route):
         raise TypeError("route must be an ExpertRoute (route_experts's), got %r" % type(route).__name__)
 
 
-def _validate_experts(x, q, scales, route, bias, gated, gather, out, device):
+def _validate_experts(x, q, scales, route, bias, gated, gather, out, device, dtype=None):
     import torch
     check = _pkg._check
+    if dtype is None:
+        dtype = torch.float16
+    if dtype not in (torch.float16, torch.float32):
+        raise TypeError("dtype must be torch.float16 or torch.float32, got %r" % (dtype,))
     check(x, "x", torch.float16, ndim=2, device=device)
     x_rows, k = x.shape
     _check_route(route)
@@ -425,59 +431,68 @@ def _validate_experts(x, q, scales, route, bias, gated, gather, out, device):
         raise ValueError("a gated product needs an even number of channels, got %d" % n)
     shape = (entries, n // 2 if gated else n)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float16, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
     else:
-        check(out, "out", torch.float16, shape=shape, device=device)
+        check(out, "out", dtype, shape=shape, device=device)
     return x_rows, k, top_k, entries, experts, n, out
 
 
 def w8a16_experts(x, q, scales, route: ExpertRoute, bias=None, activation=None, gated: bool = False, gather: bool = True,
-                  out=None):
+                  out=None, dtype=None):
     """w8a16_linear of each entry's row with its expert's weight: x fp16 [T, K]
     (a row a token), or without ``gather`` [T * top_k, K] (a row an entry, in the
     route's order), q int8 [E, N, K], scales fp16 [E, N], bias fp16 [E, N]
-    -> fp16 [T * top_k, N or, gated, N / 2] in the route's order; rows behind
-    the last entry are zero."""
+    -> [T * top_k, N or, gated, N / 2] in the route's order; rows behind the last
+    entry are zero.  ``dtype``: torch.float16, or torch.float32 for entries that
+    experts_combine adds unrounded; by default out's, else fp16."""
     torch = _loaded()
     act = _activation(activation)
     f16, i32 = torch.float16, torch.int32
+    if dtype is None:
+        dtype = torch.float32 if getattr(out, "dtype", f16) is torch.float32 else f16
     try:
         index = x.get_device()
         x_rows, k = x.shape
         tokens, top_k = route.ids.shape
         entries = tokens * top_k
         experts, n, _ = q.shape
-        fine = (out is None and index >= 0 and x.dtype is f16 and x.is_contiguous() and x_rows == (tokens if gather else entries)
+        fine = (out is None and (dtype is f16 or dtype is torch.float32) and index >= 0 and x.dtype is f16
+                and x.is_contiguous() and x_rows == (tokens if gather else entries)
                 and _fits(q, torch.int8, (experts, n, k), index) and _fits(scales, f16, (experts, n), index)
                 and _fits(route.offsets, i32, (experts + 1,), index) and _fits(route.rows, i32, (entries,), index)
                 and (bias is None or _fits(bias, f16, (experts, n), index)) and not (gated and n % 2))
     except (AttributeError, TypeError, ValueError):
         fine = False
     if fine:
-        y = torch.empty(entries, n // 2 if gated else n, dtype=f16, device=x.device)
+        y = torch.empty(entries, n // 2 if gated else n, dtype=dtype, device=x.device)
     else:
         device = _pkg._require_gpu(x, "x")
-        x_rows, k, top_k, entries, experts, n, y = _validate_experts(x, q, scales, route, bias, gated, gather, out, device)
+        x_rows, k, top_k, entries, experts, n, y = _validate_experts(x, q, scales, route, bias, gated, gather, out, device, dtype)
         index = x.get_device()
     if index != _kv._current_device():
-        return _pkg._on_device(index, w8a16_experts, x, q, scales, route, bias, activation, gated, gather, out)
-    status = _pkg.library().qw_w8a16_experts(
-        x.data_ptr(), x_rows, 1 if gather else 0, q.data_ptr(), scales.data_ptr(), _ptr(bias), act, 1 if gated else 0,
-        route.offsets.data_ptr(), route.rows.data_ptr(), entries, top_k, y.data_ptr(), experts, n, k, _kv._raw_stream(index))
+        return _pkg._on_device(index, w8a16_experts, x, q, scales, route, bias, activation, gated, gather, out, dtype)
+    lib = _pkg.library()
+    args = (x.data_ptr(), x_rows, 1 if gather else 0, q.data_ptr(), scales.data_ptr(), _ptr(bias), act, 1 if gated else 0,
+            route.offsets.data_ptr(), route.rows.data_ptr(), entries, top_k, y.data_ptr(), experts, n, k)
+    if dtype is f16:
+        status = lib.qw_w8a16_experts(*args, _kv._raw_stream(index))
+    else:
+        status = lib.qw_w8a16_experts_f32(*args, 0, 0, _kv._raw_stream(index))
     if status:
-        _raise(status, "qw_w8a16_experts")
+        _raise(status, "qw_w8a16_experts" if dtype is f16 else "qw_w8a16_experts_f32")
     return y
 
 
 def _validate_combine(y, route, residual, out, device):
     import torch
     check = _pkg._check
-    check(y, "y", torch.float16, ndim=2, device=device)
+    f32 = isinstance(y, torch.Tensor) and y.dtype == torch.float32
+    check(y, "y", torch.float32 if f32 else torch.float16, ndim=2, device=device)
     n = y.shape[1]
     _check_route(route)
     check(route.places, "route.places", torch.int32, ndim=2, device=device)
     tokens, top_k = route.places.shape
-    check(y, "y", torch.float16, shape=(tokens * top_k, n), device=device)
+    check(y, "y", y.dtype, shape=(tokens * top_k, n), device=device)
     check(route.weights, "route.weights", torch.float32, shape=(tokens, top_k), device=device)
     if residual is not None:
         check(residual, "residual", torch.float16, shape=(tokens, n), device=device)
@@ -489,7 +504,7 @@ def _validate_combine(y, route, residual, out, device):
 
 
 def experts_combine(y, route: ExpertRoute, residual=None, out=None):
-    """residual plus the weighted sum of each token's entries: y fp16
+    """residual plus the weighted sum of each token's entries: y fp16 or fp32
     [T * top_k, N] in the route's order, residual fp16 [T, N] (may be ``out``)
     -> fp16 [T, N].  A token of no expert keeps its residual, or is zero."""
     torch = _loaded()
@@ -498,7 +513,8 @@ def experts_combine(y, route: ExpertRoute, residual=None, out=None):
         index = y.get_device()
         entries, n = y.shape
         tokens, top_k = route.places.shape
-        fine = (out is None and index >= 0 and entries == tokens * top_k and y.dtype is f16 and y.is_contiguous()
+        fine = (out is None and index >= 0 and entries == tokens * top_k and (y.dtype is f16 or y.dtype is torch.float32)
+                and y.is_contiguous()
                 and _fits(route.places, torch.int32, (tokens, top_k), index)
                 and _fits(route.weights, torch.float32, (tokens, top_k), index)
                 and (residual is None or _fits(residual, f16, (tokens, n), index)))
@@ -512,9 +528,10 @@ def experts_combine(y, route: ExpertRoute, residual=None, out=None):
         index = y.get_device()
     if index != _kv._current_device():
         return _pkg._on_device(index, experts_combine, y, route, residual, out)
-    status = _pkg.library().qw_experts_combine(
+    lib = _pkg.library()
+    status = (lib.qw_experts_combine if y.dtype is f16 else lib.qw_experts_combine_f32)(
         y.data_ptr(), tokens * top_k, route.places.data_ptr(), route.weights.data_ptr(), tokens, top_k, _ptr(residual),
         o.data_ptr(), n, _kv._raw_stream(index))
     if status:
-        _raise(status, "qw_experts_combine")
+        _raise(status, "qw_experts_combine" if y.dtype is f16 else "qw_experts_combine_f32")
     return o
