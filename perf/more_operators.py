@@ -264,7 +264,7 @@ def own_experts(s):
     import int8_weight_quantized_amd as qw
     route = qw.ExpertRoute(s["ids"], s["w"], s["offsets"], s["rows"], s["places"])
     if s["down"]:
-        y = qw.w8a16_experts(s["x"], s["q"], s["scales"], route, bias=s["b"], gather=False)
+        y = qw.w8a16_experts(s["x"], s["q"], s["scales"], route, bias=s["b"], gather=False, dtype=torch.float32)
         return {"out": qw.experts_combine(y, route, residual=s["res"])}
     return {"y": qw.w8a16_experts(s["x"], s["q"], s["scales"], route, bias=s["b"], activation="silu" if s["gated"] else None,
                                   gated=s["gated"])}
