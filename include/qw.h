@@ -966,7 +966,8 @@ QW_API int64_t qw_w8a8_linear_workspace(int64_t m, int64_t n, int64_t k, int gat
  *   w = s [/ the sum of its s]  * scale
  *
  * Ties go to the lowest index.  The choice and the weights are computed in
- * binary64; the weights are rounded to binary32.  A logit (or choice) that is
+ * binary64, subnormal numbers included; the weights are rounded to binary32, and
+ * are 0 where all of a token's s are.  A logit (or choice) that is
  * -infinity or NaN is no expert's: a token with fewer than top_k others has
  * ids -1 and weights 0 in the places behind them (a row of -infinity: a token
  * that goes nowhere).  +infinity counts as the largest finite number.

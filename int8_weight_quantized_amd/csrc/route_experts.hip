@@ -187,31 +187,34 @@ __device__ __forceinline__ double sum_of(double v)
     return v;
 }
 
-// exp(x), 0 for x < -700; x <= 700.  x = n ln 2 + r, and exp(r) by its series
-// up to r^13 (|r| < 0.347: what is left out is below 2^-57).  The library's
+// exp(x) for x from kLeast to 0, subnormal results included.  x = n ln 2
+// + r with ln 2 in two parts (Cody and Waite's reduction), and exp(r) by its
+// series up to r^13 (|r| < 0.347: what is left out is below 2^-57).  The library's
 // function and its division took more than twice as long.
+constexpr double kLeast = -747.0; // (exp(-745.2) rounds to 0; larger |x| would leave n's range)
 __device__ __forceinline__ double exp_f64(double x)
 {
     constexpr double kSeries[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
                                     1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600, 1.0 / 6227020800};
     const double n = rint(x * 1.4426950408889634);
-    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x)); // ln 2 in two parts
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
     double p = kSeries[13];
 #pragma unroll
     for (int i = 12; i >= 0; --i)
         p = fma(p, r, kSeries[i]);
-    return x < -700.0 ? 0.0 : __builtin_amdgcn_ldexp(p, (int)n);
+    return __builtin_amdgcn_ldexp(p, (int)n);
 }
 
-// 1 / (1 + exp(-x)), 0 for x < -700: the reciprocal by two steps of Newton's
+// 1 / (1 + exp(-x)), for negative x as exp(x) / (1 + exp(x)), which keeps its bits
+// where exp(-x) leaves the range: the reciprocal by two steps of Newton's
 // iteration from the hardware's estimate.
 __device__ __forceinline__ double sigmoid_f64(double x)
 {
-    const double d = 1.0 + exp_f64(-fmin(fmax(x, -700.0), 700.0));
+    const double e = exp_f64(fmax(-fabs(x), kLeast)), d = 1.0 + e;
     double r = __builtin_amdgcn_rcp(d);
     r = fma(fma(-d, r, 1.0), r, r);
     r = fma(fma(-d, r, 1.0), r, r);
-    return x < -700.0 ? 0.0 : r;
+    return x < 0.0 ? e * r : r;
 }
 
 template <int DT>
@@ -286,7 +289,7 @@ __device__ __forceinline__ void choose_one_by_one(const RouteArgs &a, int64_t ro
         double sum = 0.0;
 #pragma unroll 1
         for (int e = first; e < end; ++e)
-            sum += exp_f64(fmax((double)eligible(logit<DT>(a.logits, row + e)) - most, -701.0));
+            sum += exp_f64(fmax((double)eligible(logit<DT>(a.logits, row + e)) - most, kLeast));
         total = sum_of<L>(sum);
     }
 #pragma unroll 1
@@ -294,7 +297,7 @@ __device__ __forceinline__ void choose_one_by_one(const RouteArgs &a, int64_t ro
         const double l = (double)eligible(logit<DT>(a.logits, row + e));
         double c = l;
         if (a.bias) {
-            const double v = (a.sigmoid ? sigmoid_f64(l) : exp_f64(fmax(l - most, -701.0)) / total) + (double)a.bias[e];
+            const double v = (a.sigmoid ? sigmoid_f64(l) : exp_f64(fmax(l - most, kLeast)) / total) + (double)a.bias[e];
             c = l > kNone && v > kNone ? v : kNone; // (a NaN is not chosen)
         }
         choices[e] = live ? c : kNone;
@@ -567,13 +570,13 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t token, bool l
         double sum = 0.0;
 #pragma unroll 1
         for (int e = lane * P; e < min(lane * P + P, a.experts); ++e)
-            sum += exp_f64(fmax((double)eligible(logit<DT>(a.logits, row + e)) - most, -701.0)); // (0 where there is none)
+            sum += exp_f64(fmax((double)eligible(logit<DT>(a.logits, row + e)) - most, kLeast)); // (0 where there is none)
         total = sum_of<L>(sum);
     }
     __builtin_amdgcn_wave_barrier();
     const int id = live && lane < a.top_k ? chosen.id[lane] : -1; // (top_k <= L)
     const double v = id >= 0 ? (double)chosen.logit[lane] : 0.0;
-    const double e = a.sigmoid ? sigmoid_f64(v) : exp_f64(fmax(v - most, -701.0));
+    const double e = a.sigmoid ? sigmoid_f64(v) : exp_f64(fmax(v - most, kLeast));
     double w = id >= 0 ? e : 0.0;
     if (a.renormalize)
         total = sum_of<L>(w);
