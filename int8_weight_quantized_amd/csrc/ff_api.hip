@@ -419,7 +419,7 @@ QW_API qw_status qw_route_experts(const void *logits, int dtype, int64_t tokens,
     a.groups = (int)groups;
     a.top_groups = (int)top_groups;
     a.renormalize = renormalize;
-    a.scale = (float)scale;
+    a.scale = scale;
     a.ids = ids;
     a.weights = weights;
     a.offsets = offsets;

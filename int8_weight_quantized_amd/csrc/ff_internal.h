@@ -23,7 +23,7 @@ struct RouteArgs {
     const float *bias;  // [experts], or null
     int64_t tokens;
     int experts, top_k, sigmoid, groups, top_groups, renormalize;
-    float scale;
+    double scale;
     int32_t *ids;      // [tokens][top_k]
     float *weights;    // [tokens][top_k]
     int32_t *offsets;  // [experts + 1]

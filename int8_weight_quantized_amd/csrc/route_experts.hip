@@ -580,7 +580,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t token, bool l
     double w = id >= 0 ? e : 0.0;
     if (a.renormalize)
         total = sum_of<L>(w);
-    w = total > 0.0 ? w / total * (double)a.scale : 0.0;
+    w = total > 0.0 ? w / total * a.scale : 0.0;
     if (live && lane < a.top_k) {
         a.weights[token * a.top_k + lane] = (float)w;
         a.ids[token * a.top_k + lane] = id;

@@ -74,3 +74,20 @@ def test_scores_that_are_zero(scoring):
     assert r.ids.tolist() == [[0, 1, 3, 4]] * 5 and not r.weights.any()
     r = qw.route_experts(x, 4, scoring)
     assert r.ids.tolist() == [[2, 7, 8, 9]] * 5 and r.weights.tolist() == [[1.0, 0.0, 0.0, 0.0]] * 5
+
+
+@pytest.mark.parametrize("scale", [0.1, 2.446, 1e39, -3.0, 1e-41, 0.0])
+def test_scale(scale):
+    """A factor that binary32 does not hold, or not exactly, counts as it is: one
+    rounding to 32 bits, that of the weight."""
+    gen = torch.Generator()
+    gen.manual_seed(3)
+    x = torch.randn(400, 64, generator=gen)
+    x[:, 8:] = -1e4  # (not chosen)
+    r = qw.route_experts(x.to(GPU), 8, "sigmoid", renormalize=False, scale=scale)
+    w = torch.sigmoid(x.double()).gather(1, r.ids.long().cpu()) * scale
+    got = r.weights.cpu().double()
+    inf = w.abs() > torch.finfo(F32).max
+    assert torch.equal(got.isinf(), inf) and (not inf.any() or scale > 1e38)
+    # half a step of 2^-24, or of the subnormal numbers' 2^-149
+    assert ((got - w).abs() <= 1.01 * 2.0 ** -24 * w.abs() + 2.0 ** -150)[~inf].all()
