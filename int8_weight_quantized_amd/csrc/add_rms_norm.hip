@@ -129,8 +129,28 @@ __global__ __launch_bounds__(W * kWave) void add_rms_norm_kernel(AddNormArgs a)
 template <int DT, bool CODES, int W, int V>
 hipError_t launch(const AddNormArgs &a, hipStream_t stream)
 {
-    add_rms_norm_kernel<DT, CODES, W, V><<<dim3((unsigned)a.tokens), dim3(W * kWave), 0, stream>>>(a);
-    return hipGetLastError();
+    // (a grid holds fewer than 2^32 threads: more rows go in several launches)
+    constexpr int64_t kMost = (int64_t(1) << 31) / (W * kWave);
+    for (int64_t first = 0; first < a.tokens; first += kMost) {
+        AddNormArgs part = a;
+        part.x += first * a.x_stride;
+        if (a.residual) {
+            part.residual += first * a.residual_stride;
+            part.h += first * a.h_stride;
+        }
+        if (CODES) {
+            part.q += first * a.k;
+            part.scales += first;
+        } else {
+            part.y += first * a.k;
+        }
+        const int64_t rows = a.tokens - first < kMost ? a.tokens - first : kMost;
+        add_rms_norm_kernel<DT, CODES, W, V><<<dim3((unsigned)rows), dim3(W * kWave), 0, stream>>>(part);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 template <int DT, bool CODES>

@@ -1,0 +1,51 @@
+"""Feed-forward calls of so many rows or channels that one grid does not hold a
+thread for each piece of work (2^32 threads)."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+qw = pytest.importorskip("int8_weight_quantized_amd")
+
+F16 = torch.float16
+GPU = "cuda:0"
+
+
+@pytest.fixture(autouse=True)
+def memory():
+    if torch.cuda.get_device_properties(0).total_memory < (160 << 30):
+        pytest.skip("needs 160 GiB")
+    yield
+    torch.cuda.empty_cache()
+
+
+def ints(seed, shape, top, dtype):
+    g = torch.Generator(device=GPU)
+    g.manual_seed(seed)
+    return torch.randint(-top, top + 1, shape, generator=g, device=GPU, dtype=torch.int8).to(dtype)
+
+
+@pytest.mark.parametrize("quantize", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_rows(residual, quantize):
+    """256 threads a row: 2^24 rows are 2^32 threads.  Every row as in calls of
+    parts of them."""
+    T, K = (1 << 24) + 37, 16
+    print("norm", T, K, residual, quantize, flush=True)
+    x = ints(1, (T, K), 100, F16)
+    r = ints(2, (T, K), 100, F16) if residual else None
+    w = torch.linspace(0.5, 2, K, device=GPU).half()
+    whole = qw.add_rms_norm(x, w, residual=r, quantize=quantize)
+    cut = [0, 5000001, (1 << 23) - 1, (1 << 23) + 3, T - 1, T]
+    for a, b in zip(cut, cut[1:]):
+        part = qw.add_rms_norm(x[a:b], w, residual=None if r is None else r[a:b], quantize=quantize)
+        for one, other in zip(whole, part):
+            assert torch.equal(one[a:b], other)
+    h = x.double() if r is None else x.double() + r.double()
+    y = h * w.double() / (h.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    if quantize:
+        got = whole[0].double() * whole[1].double()[:, None]
+        assert ((got - y).abs() <= 0.51 * whole[1].double()[:, None]).all()
+    else:
+        assert ((whole[0].double() - y).abs() <= 2.0 ** -10.9 * y.abs() + 2.0 ** -24).all()
