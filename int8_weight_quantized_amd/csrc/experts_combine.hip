@@ -69,9 +69,9 @@ struct Entries<WHOLE, true> {
 };
 
 template <bool WHOLE, bool F32>
-__global__ __launch_bounds__(kThreads) void experts_combine_kernel(CombineArgs a, int pieces)
+__global__ __launch_bounds__(kThreads) void experts_combine_kernel(CombineArgs a, int pieces, int64_t first)
 {
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t id = (first + blockIdx.x) * kThreads + threadIdx.x;
     const int64_t token = id / pieces;
     if (token >= a.tokens)
         return;
@@ -122,11 +122,17 @@ hipError_t launch_experts_combine(const CombineArgs &a, hipStream_t stream)
 {
     const int64_t pieces = (a.n + 7) / 8;
     const int64_t blocks = (a.tokens * pieces + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
+    // (a grid holds fewer than 2^32 threads: more go in several launches)
+    constexpr int64_t kMost = (int64_t(1) << 31) / kThreads;
     auto launch = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, (int)pieces);
-        return hipGetLastError();
+        for (int64_t first = 0; first < blocks; first += kMost) {
+            const int64_t count = blocks - first < kMost ? blocks - first : kMost;
+            hipLaunchKernelGGL(kernel, dim3((unsigned)count), dim3(kThreads), 0, stream, a, (int)pieces, first);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess)
+                return e;
+        }
+        return hipSuccess;
     };
     if (a.f32)
         return a.n % 8 == 0 ? launch(experts_combine_kernel<true, true>) : launch(experts_combine_kernel<false, true>);

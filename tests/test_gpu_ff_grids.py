@@ -49,3 +49,25 @@ def test_norm_rows(residual, quantize):
         assert ((got - y).abs() <= 0.51 * whole[1].double()[:, None]).all()
     else:
         assert ((whole[0].double() - y).abs() <= 2.0 ** -10.9 * y.abs() + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_combine_pieces(f32):
+    """A thread for 8 columns of a token: 2^26 tokens of 512 are 2^32 threads.
+    The tokens' places are a few rows."""
+    T, n, rows = (1 << 26) + 5, 512, 64
+    print("combine", T, n, f32, flush=True)
+    y = ints(3, (rows, n), 100, torch.float32 if f32 else F16)
+    g = torch.Generator(device=GPU)
+    g.manual_seed(4)
+    places = torch.randint(-1, rows, (T, 1), generator=g, device=GPU, dtype=torch.int32)
+    weights = torch.full((T, 1), 0.5, device=GPU)
+    out = torch.full((T, n), 7.0, dtype=F16, device=GPU)
+    call = qw.library().qw_experts_combine_f32 if f32 else qw.library().qw_experts_combine
+    st = call(y.data_ptr(), rows, places.data_ptr(), weights.data_ptr(), T, 1, None, out.data_ptr(), n,
+              torch.cuda.current_stream().cuda_stream)
+    assert st == 0, qw.status_string(st)
+    for at in range(0, T, 1 << 22):
+        p = places[at:at + (1 << 22), 0].long()
+        want = torch.where((p < 0)[:, None], 0.0, y.float()[p.clamp(min=0)] * 0.5)
+        assert torch.equal(out[at:at + (1 << 22)].float(), want)
