@@ -69,7 +69,9 @@ hipError_t launch_split(const LinearArgs &a, const Experts &ex, int64_t row_tile
 template <int MT, bool A8, int EPI>
 bool launch_shared(const LinearArgs &a, hipStream_t stream, hipError_t &result)
 {
-    if (a.m <= 4 || a.m > 16 * MT || a.k > (1 << 30)) // (its loads ahead count past k in 32 bits)
+    // (its loads ahead count past k in 32 bits, and its grid of up to 8 n threads
+    // has to stay below 2^32)
+    if (a.m <= 4 || a.m > 16 * MT || a.k > (1 << 30) || a.n > (1 << 28))
         return false;
     const Experts none = {};
     const int64_t cus = device_cu_count(), wide = (a.n + 127) / 128, narrow = (a.n + 63) / 64;

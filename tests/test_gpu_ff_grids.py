@@ -71,3 +71,29 @@ def test_combine_pieces(f32):
         p = places[at:at + (1 << 22), 0].long()
         want = torch.where((p < 0)[:, None], 0.0, y.float()[p.clamp(min=0)] * 0.5)
         assert torch.equal(out[at:at + (1 << 22)].float(), want)
+
+
+@pytest.mark.parametrize("m,n,gated,a8", [(5, (1 << 29) + 64, False, False), (5, (1 << 29) + 64, False, True),
+                                          (20, (1 << 30) + 128, False, False), (5, (1 << 30) + 128, True, False)])
+def test_channels(m, n, gated, a8):
+    """Eight (or, with 128 rows a workgroup, four) threads a channel where waves
+    share the activations."""
+    k = 16
+    print("channels", m, n, gated, a8, flush=True)
+    q = ints(5, (n, k), 127, torch.int8)
+    s = torch.full((n,), 2.0 ** -6, dtype=F16, device=GPU)
+    x = ints(6, (m, k), 3, torch.int8 if a8 else F16)
+    columns = n // 2 if gated else n
+    y = torch.full((m, columns), float("nan"), dtype=F16, device=GPU)
+    if a8:
+        qw.w8a8_linear(x, torch.ones(m, dtype=F16, device=GPU), q, s, out=y)
+    else:
+        qw.w8a16_linear(x, q, s, activation="relu" if gated else None, gated=gated, out=y)
+    for c in range(0, columns, 1 << 25):
+        e = min(columns, c + (1 << 25))
+
+        def product(lo):
+            # (integers below 2^24 and powers of two: exact in fp32)
+            return x.float() @ q[lo + c:lo + e].float().t() * 2.0 ** -6
+        want = product(0).clamp(min=0) * product(columns) if gated else product(0)
+        assert torch.equal(y[:, c:e], want.half())
