@@ -848,8 +848,9 @@ typedef enum qw_activation {
  *   q       int8 [tokens][k] (written)
  *   scales  fp16 bits [tokens] (written)
  *
- * Rows with values that are not finite, or above 2^60, give unspecified
- * outputs (of that row).
+ * Rows with values that are not finite, or above 2^60, and rows whose mean of h^2
+ * and eps both lie below 2^-100 give unspecified outputs (of that row); rows of
+ * zeros do so with eps == 0 alone.
  *
  * Errors: QW_ERROR_INVALID_VALUE (null pointer, h null with a residual or the
  * reverse, negative size, k <= 0, a stride below k, unknown dtype, eps negative

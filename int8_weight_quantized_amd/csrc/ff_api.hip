@@ -1,6 +1,7 @@
 // ff_api.hip -- the C ABI of the feed-forward operators: argument checks on the
 // host, kernel selection, launch on the caller's stream.  Nothing is allocated
 // here, and a rejected call launches nothing and writes nothing.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -253,7 +254,8 @@ qw_status add_norm(qw::AddNormArgs a, int dtype, double eps, bool codes, void *s
             (!on_res && rows_meet(a.h, a.h_stride, a.residual, a.residual_stride, k, T)))
             return QW_ERROR_INVALID_VALUE;
     }
-    a.eps = (float)eps;
+    // (an eps that binary32 loses still keeps a row of zeros from 0 / 0)
+    a.eps = eps > 0.0 && eps < FLT_MIN ? FLT_MIN : (float)eps;
     return status_of(qw::launch_add_rms_norm(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
