@@ -18,8 +18,10 @@
 // with a residual / and codes, as launched and with four waves of four vectors:
 // 1 x 4096 2.5 / 2.7 and 3.1 / 3.4, 256 x 8192 4.2 / 4.6 and 5.0 / 5.4, 8192 x
 // 4096 38.9 / 35.0 and 40.2 / 38.8, 8192 x 8192 91 / 83 (5.9 and 5.6 TB/s) and
-// 95 / 89.  4096 x 16384 with two vectors 97 / 87, with eight 104 / 109.  2048 x
-// 65536 207 / 204.
+// 95 / 89.  4096 x 16384 with two vectors 97 / 87, with eight 104 / 109.  Beyond,
+// eight for all: 4096 x 20480 128 / 129, 2048 x 32768 107 / 106, 2048 x 65536
+// 207 / 203 (5.0 to 5.3 and 4.4 to 4.6 TB/s).  Short rows leave waves without work
+// (four a row up to 2048 elements): 16384 x 256 11 / 17, 512 13 / 18, 1024 21 / 22.
 #include "ff_internal.h"
 #include "kv_device.h"
 

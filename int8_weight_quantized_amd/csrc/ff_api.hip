@@ -36,7 +36,9 @@ bool known_tile(int tile, bool a8)
 // 31, 61 / 35, 93 / 44, 143 / 61; 512 rows 26 / 45, 39 / 48, 63 / 54, 94 / 57, 146 / 73;
 // 2048 rows 57 / 60, 90 / 78, 112 / 92, 173 / 131, 268 / 184; W8A16 256 rows 34 / 36,
 // 47 / 36, 70 / 42, 139 / 55, 206 / 75; 512 rows 35 / 44, 56 / 51, 71 / 57, 139 / 75,
-// 206 / 96; 2048 rows 82 / 85, 119 / 111, 151 / 137, 245 / 211, 361 / 301.
+// 206 / 96; 2048 rows 82 / 85, 119 / 111, 151 / 137, 245 / 211, 361 / 301.  (Of
+// other n nothing was measured; W8A8 with 256 rows and k = 6144 would gain and is
+// left out.)
 int split_parts(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
 {
     const int64_t columns = gated ? n / 2 : n, bn = gated ? 128 : 256;
@@ -83,8 +85,9 @@ LinearPlan plan_linear(int64_t m, int64_t n, int64_t k, bool gated, bool a8)
         p.tile = 0;
     if (p.path == QW_PATH_SKINNY)
         p.splits = skinny_parts(m, n, k, gated, a8);
-    // (rounding m up to 256 rows costs at most a tenth over 64, as for the
-    // ping-pong tile without a split)
+    // (where rounding m up to 256 rows costs at most a tenth over 64, as for the
+    // ping-pong tile without a split.  The split would gain beyond: n = 4096, k =
+    // 13696, 64 to 192 rows 90 us, in 8 parts 44 to 47, W8A8 61 and 33)
     const int64_t rows256 = (m + 255) / 256 * 256, rows64 = (m + 63) / 64 * 64;
     if (p.path == QW_PATH_MFMA && p.tile == 0 && k <= qw::kPingPongMaxK && 10 * rows256 <= 11 * rows64) {
         p.splits = split_parts(m, n, k, gated, a8);
