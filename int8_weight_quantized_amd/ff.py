@@ -443,13 +443,13 @@ def w8a16_experts(x, q, scales, route: ExpertRoute, bias=None, activation=None, 
     (a row a token), or without ``gather`` [T * top_k, K] (a row an entry, in the
     route's order), q int8 [E, N, K], scales fp16 [E, N], bias fp16 [E, N]
     -> [T * top_k, N or, gated, N / 2] in the route's order; rows behind the last
-    entry are zero.  ``dtype``: torch.float16, or torch.float32 for entries that
-    experts_combine adds unrounded; by default out's, else fp16."""
+    entry are zero.  ``dtype``: torch.float16 (the default), or torch.float32 for
+    entries that experts_combine adds unrounded."""
     torch = _loaded()
     act = _activation(activation)
     f16, i32 = torch.float16, torch.int32
     if dtype is None:
-        dtype = torch.float32 if getattr(out, "dtype", f16) is torch.float32 else f16
+        dtype = f16
     try:
         index = x.get_device()
         x_rows, k = x.shape

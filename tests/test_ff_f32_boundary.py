@@ -52,7 +52,7 @@ def test_binding():
 @pytest.mark.parametrize("call", [
     lambda: qw.w8a16_experts(second((4, 32)), second((3, 8, 32), torch.int8), second((3, 8)), host.route_on_second(), dtype=F32),
     lambda: qw.w8a16_experts(second((8, 32)), second((3, 8, 32), torch.int8), second((3, 8)), host.route_on_second(), gather=False,
-                             out=second((8, 8), F32)),
+                             out=second((8, 8), F32), dtype=F32),
     lambda: qw.experts_combine(second((8, 16), F32), host.route_on_second(), residual=second((4, 16))),
 ])
 def test_operands_on_another_device_than_the_current_one(devices, call):

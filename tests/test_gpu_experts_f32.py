@@ -83,7 +83,9 @@ def test_one_rounding(tokens, experts, top_k, n, k, residual):
     assert y.dtype is F32
     assert_rounded(qw.experts_combine(y, route, residual=r), total, off)
     out = torch.empty_like(y)
-    assert qw.w8a16_experts(x, q, s, route, bias=b, gather=False, out=out) is out and torch.equal(out, y)
+    with pytest.raises(TypeError):
+        qw.w8a16_experts(x, q, s, route, bias=b, gather=False, out=out)  # (fp16 unless it is asked for)
+    assert qw.w8a16_experts(x, q, s, route, bias=b, gather=False, out=out, dtype=F32) is out and torch.equal(out, y)
 
 
 def test_entries_beyond_fp16():
